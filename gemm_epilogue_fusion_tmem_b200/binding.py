@@ -93,6 +93,14 @@ def library() -> ctypes.CDLL:
             "coda_grg_bwd_unfused": (I, [P] * 15 + [I, I, I, I, P, S, P]),
             "coda_grg_fwd_prefolded_static": (I, [P] * 8 + [I, I, I, I, F, P]),
             "coda_static_status_query": (I, [P, ctypes.POINTER(ctypes.c_uint32)]),
+            "coda_quant_fp8": (I, [P] * 7 + [I, I, I, P]),
+            "coda_quant_fp8_blocks": (I, [P, P, P, I, I, I, P]),
+            "coda_gemm_fp8": (I, [P] * 5 + [I] * 10 + [P, S, P]),
+            "coda_gemm_swiglu_fp8": (I, [P] * 8 + [I, I, I, P, S, P]),
+            "coda_swiglu_fp8_bwd": (I, [P] * 9 + [I, I, I, P]),
+            "coda_rmsnorm_fp8_fwd": (I, [P] * 7 + [I, I, F, P]),
+            "coda_rmsnorm_fp8_bwd_workspace_bytes": (S, [I, I]),
+            "coda_rmsnorm_fp8_bwd": (I, [P] * 7 + [I, I, P, S, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -213,10 +221,13 @@ def set_wait_limit_ns(ns: int) -> None:
     library().coda_set_wait_limit_ns(int(ns))
 
 
-# Kernel ids of the timing hook (coda_profile_arm): GEMMs by epilogue, light passes from 16.
+# Kernel ids of the timing hook (coda_profile_arm): GEMMs by epilogue, light passes from 16,
+# the 8-bit operators from 32.
 EPI_STORE, EPI_RESID_RMS, EPI_SWIGLU, EPI_DN, EPI_SWIGLU_BWD, EPI_XENT, EPI_XENT_BWD, EPI_ROPE = range(8)
 (KERNEL_FOLD_GAIN, KERNEL_RMS_ROWREDUCE, KERNEL_SWIGLU_BWD_ROWSTAT, KERNEL_COL_REDUCE, KERNEL_ROWCOEF_REDUCE,
  KERNEL_XENT_REDUCE, KERNEL_ROPE_UNROTATE) = range(16, 23)
+(KERNEL_GEMM_FP8, KERNEL_GEMM_SWIGLU_FP8, KERNEL_QUANT_FP8, KERNEL_SWIGLU_FP8_BWD, KERNEL_RMSNORM_FP8_FWD,
+ KERNEL_RMSNORM_FP8_BWD) = range(32, 38)
 
 
 def profile_arm(kernel: int, start=None, stop=None) -> None:
@@ -660,4 +671,253 @@ def swiglu_bwd_unfused(dOut, X, Wgu, Wdown, Y, AB, out: dict | None = None, ws: 
     _check(lib.coda_swiglu_bwd_unfused(_ptr(dOut), _ptr(X), _ptr(Wgu), _ptr(Wdown), _ptr(Y), _ptr(AB), _ptr(o["dX"]),
                                        _ptr(o["dWgu"]), _ptr(o["dWdown"]), M, d, F, ws.ptr(), ws.nbytes, _stream()),
            "coda_swiglu_bwd_unfused")
+    return o
+
+
+# ------------------------------------------------------------------ 8-bit operands
+
+_FP8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+
+
+def _cdiv(a: int, b: int) -> int:
+    return -(-a // b)
+
+
+def _fp8(dtype, name: str) -> int:
+    if dtype not in _FP8:
+        raise TypeError(f"{name} must be torch.float8_e4m3fn or torch.float8_e5m2, got {dtype}")
+    return _FP8[dtype]
+
+
+def _req2(t, name: str) -> tuple:
+    """Rows and columns of the matrix that fixes an entry point's sizes."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
+    return tuple(t.shape)
+
+
+def _same_device(dev, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+
+
+def _give(o: dict, key: str, shape, dtype, dev) -> torch.Tensor:
+    """The caller's output tensor o[key], checked, or a new one."""
+    if key not in o:
+        o[key] = torch.empty(shape, dtype=dtype, device=dev)
+    _req(o[key], key, dtype, shape)
+    _same_device(dev, **{key: o[key]})
+    return o[key]
+
+
+_status_ws: dict = {}
+
+
+def _status_workspace(dev) -> Workspace:
+    """The device's status word for calls that need no other scratch.  It is
+    never replaced, so captured graphs may keep its address; a call that is
+    itself being captured before the first eager one gets a word of its own in
+    the graph."""
+    ws = _status_ws.get(dev)
+    if ws is None:
+        ws = Workspace(256, dev)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(dev).synchronize()  # zeroed for every stream from here on
+            _status_ws[dev] = ws
+    return ws
+
+
+def fp8_status(device=None) -> tuple[int, int]:
+    """Synchronise the current stream and return (status, detail) of the 8-bit
+    products that were given no workspace on this device."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with torch.cuda.device(dev):
+        return _status_workspace(dev).query()
+
+
+def quant_fp8(X, rows: bool = True, cols: bool = False, rowvec=None, colvec=None, fmt=torch.float8_e4m3fn,
+              out: dict | None = None) -> dict:
+    """X (bf16 [R, C], optionally scaled by rowvec fp32 [R] and colvec bf16 [C])
+    in 8 bits with a scale per 128 values, in one pass; see coda_quant_fp8.
+
+    rows: Qr [R, C], Sr [ceil(C/128), R], one scale per row and 128 columns;
+    cols: Qc [R, C], Sc [ceil(R/128), C], one scale per column and 128 rows."""
+    R, C = _req2(X, "X")
+    _req(X, "X")
+    f = _fp8(fmt, "fmt")
+    if not rows and not cols:
+        raise ValueError("rows or cols (or both) must be asked for")
+    if rowvec is not None:
+        _req(rowvec, "rowvec", torch.float32, (R,))
+    if colvec is not None:
+        _req(colvec, "colvec", shape=(C,))
+    dev = X.device
+    _same_device(dev, rowvec=rowvec, colvec=colvec)
+    o = dict(out or {})
+    if rows:
+        _give(o, "Qr", (R, C), fmt, dev), _give(o, "Sr", (_cdiv(C, 128), R), torch.float32, dev)
+    if cols:
+        _give(o, "Qc", (R, C), fmt, dev), _give(o, "Sc", (_cdiv(R, 128), C), torch.float32, dev)
+    with torch.cuda.device(dev):
+        _check(library().coda_quant_fp8(_ptr(X), _ptr(rowvec), _ptr(colvec),
+                                        _ptr(o["Qr"] if rows else None), _ptr(o["Sr"] if rows else None),
+                                        _ptr(o["Qc"] if cols else None), _ptr(o["Sc"] if cols else None),
+                                        R, C, f, _stream()), "coda_quant_fp8")
+    return o
+
+
+def quant_fp8_blocks(W, fmt=torch.float8_e4m3fn, out: dict | None = None) -> dict:
+    """A weight W (bf16 [R, C]) in 8 bits with a scale per 128 x 128 block: Q, S
+    [ceil(R/128), ceil(C/128)]; see coda_quant_fp8_blocks."""
+    R, C = _req2(W, "W")
+    _req(W, "W")
+    f = _fp8(fmt, "fmt")
+    dev = W.device
+    o = dict(out or {})
+    _give(o, "Q", (R, C), fmt, dev), _give(o, "S", (_cdiv(R, 128), _cdiv(C, 128)), torch.float32, dev)
+    with torch.cuda.device(dev):
+        _check(library().coda_quant_fp8_blocks(_ptr(W), _ptr(o["Q"]), _ptr(o["S"]), R, C, f, _stream()),
+               "coda_quant_fp8_blocks")
+    return o
+
+
+def gemm_fp8(A, SA, B, SB, M: int, N: int, K: int, a_mn_major: bool = False, b_mn_major: bool = False,
+             b_blocks: bool = True, out_dtype=torch.bfloat16, accumulate: bool = False,
+             out: torch.Tensor | None = None, ws: Workspace | None = None) -> torch.Tensor:
+    """C[M,N] = op(A) op(B)^T over 8-bit operands; see coda_gemm_fp8.
+
+    A [M, K] with row scales, or [K, M] (a_mn_major) with column scales: SA
+    [ceil(K/128), M].  B [N, K] or [K, N] (b_mn_major), SB in 128 x 128 blocks of
+    B as stored, or (b_blocks=False) [ceil(K/128), N].  out_dtype bf16 or fp32;
+    accumulate adds to an fp32 `out`.  Without `ws`, fp8_status() reads the
+    status word."""
+    lib = library()
+    if not all(isinstance(t, torch.Tensor) for t in (A, SA, B, SB)):
+        raise TypeError("A, SA, B and SB must be torch.Tensors")
+    fa, fb = _fp8(A.dtype, "A"), _fp8(B.dtype, "B")
+    _req(A, "A", A.dtype, (K, M) if a_mn_major else (M, K))
+    _req(B, "B", B.dtype, (K, N) if b_mn_major else (N, K))
+    kb = _cdiv(K, 128)
+    _req(SA, "SA", torch.float32, (kb, M))
+    nb = _cdiv(N, 128)
+    _req(SB, "SB", torch.float32, ((kb, nb) if b_mn_major else (nb, kb)) if b_blocks else (kb, N))
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
+    if accumulate and (out is None or out_dtype != torch.float32):
+        raise ValueError("accumulate adds to an fp32 `out`: give one, with out_dtype=torch.float32")
+    dev = A.device
+    C = out if out is not None else torch.empty(M, N, dtype=out_dtype, device=dev)
+    _req(C, "C", out_dtype, (M, N))
+    _same_device(dev, SA=SA, B=B, SB=SB, C=C)
+    with torch.cuda.device(dev):
+        ws = ws or _status_workspace(dev)
+        _check(lib.coda_gemm_fp8(_ptr(A), _ptr(SA), _ptr(B), _ptr(SB), _ptr(C), M, N, K, int(a_mn_major),
+                                 int(b_mn_major), fa, fb, int(b_blocks), int(out_dtype == torch.float32),
+                                 int(accumulate), ws.ptr(), ws.nbytes, _stream()), "coda_gemm_fp8")
+    return C
+
+
+def gemm_swiglu_fp8(A, SA, Wgu, SW, save_ab: bool = True, out: dict | None = None,
+                    ws: Workspace | None = None) -> dict:
+    """Gate/up product with SwiGLU on 8-bit operands (e4m3): Y [M, F] with SY
+    [F/128, M] and, with save_ab, the checkpoint AB = [a | b] [M, 2F] with SAB
+    [2F/128, M]; see coda_gemm_swiglu_fp8."""
+    lib = library()
+    e4m3 = torch.float8_e4m3fn
+    M, K = _req2(A, "A")
+    F = _req2(Wgu, "Wgu")[0] // 2
+    _req(A, "A", e4m3), _req(Wgu, "Wgu", e4m3, (2 * F, K))
+    kb = _cdiv(K, 128)
+    _req(SA, "SA", torch.float32, (kb, M))
+    if F % 128 != 0:
+        raise CodaError(2, "coda_gemm_swiglu_fp8")
+    fb = F // 128
+    _req(SW, "SW", torch.float32, (2 * fb, kb))
+    dev = A.device
+    _same_device(dev, SA=SA, Wgu=Wgu, SW=SW)
+    o = dict(out or {})
+    _give(o, "Y", (M, F), e4m3, dev), _give(o, "SY", (fb, M), torch.float32, dev)
+    if save_ab:
+        _give(o, "AB", (M, 2 * F), e4m3, dev), _give(o, "SAB", (2 * fb, M), torch.float32, dev)
+    with torch.cuda.device(dev):
+        ws = ws or _status_workspace(dev)
+        _check(lib.coda_gemm_swiglu_fp8(_ptr(A), _ptr(SA), _ptr(Wgu), _ptr(SW), _ptr(o["Y"]), _ptr(o["SY"]),
+                                        _ptr(o["AB"] if save_ab else None), _ptr(o["SAB"] if save_ab else None),
+                                        M, K, F, ws.ptr(), ws.nbytes, _stream()), "coda_gemm_swiglu_fp8")
+    return o
+
+
+def swiglu_fp8_bwd(dY, AB, SAB, cols: bool = True, fmt=torch.float8_e4m3fn, out: dict | None = None) -> dict:
+    """SwiGLU backward from the 8-bit checkpoint: dA = [da | db] (rows form, SdA)
+    and, with cols, dAc, SdAc and Yc, SYc (columns form, the operands of the
+    weight gradients); see coda_swiglu_fp8_bwd.  fmt is dA's and dAc's type."""
+    e4m3 = torch.float8_e4m3fn
+    M, F = _req2(dY, "dY")
+    _req(dY, "dY")
+    _req(AB, "AB", e4m3, (M, 2 * F))
+    f = _fp8(fmt, "fmt")
+    if F % 128 != 0:
+        raise CodaError(2, "coda_swiglu_fp8_bwd")
+    fb, mb = F // 128, _cdiv(M, 128)
+    _req(SAB, "SAB", torch.float32, (2 * fb, M))
+    dev = dY.device
+    _same_device(dev, AB=AB, SAB=SAB)
+    o = dict(out or {})
+    _give(o, "dA", (M, 2 * F), fmt, dev), _give(o, "SdA", (2 * fb, M), torch.float32, dev)
+    if cols:
+        _give(o, "dAc", (M, 2 * F), fmt, dev), _give(o, "SdAc", (mb, 2 * F), torch.float32, dev)
+        _give(o, "Yc", (M, F), e4m3, dev), _give(o, "SYc", (mb, F), torch.float32, dev)
+    c = [_ptr(o[k] if cols else None) for k in ("dAc", "SdAc", "Yc", "SYc")]
+    with torch.cuda.device(dev):
+        _check(library().coda_swiglu_fp8_bwd(_ptr(dY), _ptr(AB), _ptr(SAB), _ptr(o["dA"]), _ptr(o["SdA"]), *c,
+                                             M, F, f, _stream()), "coda_swiglu_fp8_bwd")
+    return o
+
+
+def rmsnorm_fp8_fwd(X, g, eps: float, R=None, out: dict | None = None) -> dict:
+    """H = X + R (when R is given), r = rsqrt(mean H^2 + eps), and H r g in 8
+    bits: Q [M, d] e4m3, S [ceil(d/128), M]; returns H (with R), r, Q, S; see
+    coda_rmsnorm_fp8_fwd."""
+    M, d = _req2(X, "X")
+    _req(X, "X"), _req(g, "g", shape=(d,))
+    if R is not None:
+        _req(R, "R", shape=(M, d))
+    dev = X.device
+    _same_device(dev, g=g, R=R)
+    o = dict(out or {})
+    if R is not None:
+        _give(o, "H", (M, d), torch.bfloat16, dev)
+    _give(o, "r", (M,), torch.float32, dev)
+    _give(o, "Q", (M, d), torch.float8_e4m3fn, dev), _give(o, "S", (_cdiv(d, 128), M), torch.float32, dev)
+    with torch.cuda.device(dev):
+        _check(library().coda_rmsnorm_fp8_fwd(_ptr(X), _ptr(R), _ptr(g), _ptr(o["H"] if R is not None else None),
+                                              _ptr(o["r"]), _ptr(o["Q"]), _ptr(o["S"]), M, d, float(eps), _stream()),
+               "coda_rmsnorm_fp8_fwd")
+    return o
+
+
+def rmsnorm_fp8_bwd(dN, H, r, g, dH_in=None, out: dict | None = None, ws: Workspace | None = None) -> dict:
+    """Backward of rmsnorm_fp8_fwd (the rounding to 8 bits passes gradients
+    through): returns dH (bf16, the gradient of X and of R) and dg (fp32); see
+    coda_rmsnorm_fp8_bwd.  Without `ws` the scratch is this call's own."""
+    lib = library()
+    M, d = _req2(dN, "dN")
+    _req(dN, "dN"), _req(H, "H", shape=(M, d)), _req(r, "r", torch.float32, (M,)), _req(g, "g", shape=(d,))
+    if dH_in is not None:
+        _req(dH_in, "dH_in", shape=(M, d))
+    dev = dN.device
+    _same_device(dev, H=H, r=r, g=g, dH_in=dH_in)
+    o = dict(out or {})
+    _give(o, "dH", (M, d), torch.bfloat16, dev), _give(o, "dg", (d,), torch.float32, dev)
+    with torch.cuda.device(dev):
+        if ws is None:
+            buf = torch.empty(lib.coda_rmsnorm_fp8_bwd_workspace_bytes(M, d), dtype=torch.uint8, device=dev)
+            wp, wn = ctypes.c_void_p(buf.data_ptr()), buf.numel()
+        else:
+            wp, wn = ws.ptr(), ws.nbytes
+        _check(lib.coda_rmsnorm_fp8_bwd(_ptr(dN), _ptr(H), _ptr(r), _ptr(g), _ptr(dH_in), _ptr(o["dH"]),
+                                        _ptr(o["dg"]), M, d, wp, wn, _stream()), "coda_rmsnorm_fp8_bwd")
     return o

@@ -446,7 +446,8 @@ coda_status coda_profile_arm(int kernel, void* ev_start, void* ev_stop) {
     return CODA_OK;
   }
   const bool known = (kernel >= CODA_EPI_STORE && kernel <= CODA_EPI_ROPE) ||
-                     (kernel >= CODA_KERNEL_FOLD_GAIN && kernel <= CODA_KERNEL_ROPE_UNROTATE);
+                     (kernel >= CODA_KERNEL_FOLD_GAIN && kernel <= CODA_KERNEL_ROPE_UNROTATE) ||
+                     (kernel >= CODA_KERNEL_GEMM_FP8 && kernel <= CODA_KERNEL_RMSNORM_FP8_BWD);
   if (ev_start == nullptr || ev_stop == nullptr || !known || g_prof_n >= kProfileSlots) return CODA_ERR_INVALID_ARG;
   g_prof[g_prof_n++] = ProfileSlot{kernel, static_cast<cudaEvent_t>(ev_start), static_cast<cudaEvent_t>(ev_stop)};
   return CODA_OK;
@@ -1358,3 +1359,7 @@ extern "C" coda_status coda_static_status_query(void* stream, uint32_t* detail) 
   if (detail != nullptr) *detail = w[1];
   return static_cast<coda_status>(w[0]);
 }
+
+// ------------------------------------------------------------------ 8-bit operators
+
+#include "coda_api_fp8.cuh"

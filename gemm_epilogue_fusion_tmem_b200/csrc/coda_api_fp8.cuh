@@ -1,0 +1,449 @@
+// C-ABI entry points of the 8-bit operators (include/coda.h): argument
+// validation, tensor maps and launches.  Included at the end of coda_api.cu,
+// whose launch, device and timing-hook helpers it uses.
+#pragma once
+
+#include "coda_fp8.cuh"
+#include "coda_gemm_fp8.cuh"
+
+namespace coda {
+namespace {
+
+constexpr int kScaleBlock = 128;  // values per scale along a blocked axis
+
+// Encoded maps of the 8-bit path, cached per host thread as make_tmap's are;
+// rows of `cols` elements, `ld` elements apart.
+struct Tmap8Slot {
+  const void* base;
+  long long rows, cols, ld;
+  int dtype, box_cols, box_rows, swizzle;
+  CUtensorMap map;
+  bool valid;
+};
+constexpr int kTmap8Slots = 128;
+thread_local Tmap8Slot t_tmap8_cache[kTmap8Slots];
+
+bool make_tmap8(CUtensorMap* m, CUtensorMapDataType dtype, int elem_bytes, const void* base, long long rows,
+                long long cols, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
+  uint64_t h = reinterpret_cast<uintptr_t>(base) >> 4;
+  for (uint64_t v : {(uint64_t)rows, (uint64_t)cols, (uint64_t)box_cols * 1024 + (uint64_t)box_rows,
+                     (uint64_t)swizzle * 64 + (uint64_t)dtype})
+    h = (h ^ v) * 0x9E3779B97F4A7C15ull;
+  Tmap8Slot& s = t_tmap8_cache[(h >> 32) % kTmap8Slots];
+  if (s.valid && s.base == base && s.rows == rows && s.cols == cols && s.dtype == (int)dtype &&
+      s.box_cols == box_cols && s.box_rows == box_rows && s.swizzle == (int)swizzle) {
+    *m = s.map;
+    return true;
+  }
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)cols * elem_bytes};
+  cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  if (enc(m, dtype, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  s.base = base;
+  s.rows = rows;
+  s.cols = cols;
+  s.dtype = (int)dtype;
+  s.box_cols = box_cols;
+  s.box_rows = box_rows;
+  s.swizzle = (int)swizzle;
+  s.map = *m;
+  s.valid = true;
+  return true;
+}
+
+constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+
+// A operand [m, k]: one box of 128 k x 128 m.  B operand [n, k]: boxes of 64 n
+// (a CTA's share of one column half).
+bool operand8_map_a(CUtensorMap* m, const void* p, long long mn, long long k, bool mn_major) {
+  if (mn_major) return make_tmap8(m, kU8, 1, p, k, mn, 128, F8_BK, CU_TENSOR_MAP_SWIZZLE_128B);
+  return make_tmap8(m, kU8, 1, p, mn, k, F8_BK, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+bool operand8_map_b(CUtensorMap* m, const void* p, long long mn, long long k, bool mn_major) {
+  if (mn_major) return make_tmap8(m, kU8, 1, p, k, mn, 64, F8_BK, CU_TENSOR_MAP_SWIZZLE_64B);
+  return make_tmap8(m, kU8, 1, p, mn, k, F8_BK, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Rasterisation as pick_group, in bytes of 8-bit operands.
+int pick_group8(long long a_rows, long long b_rows, int num_m, int num_n, int k_blocks, int clusters) {
+  int side = 1;
+  while (side * side < clusters) ++side;
+  const long long budget = (long long)raster_budget_mb() << 20;
+  const long long g = std::max<long long>(side, budget / (256LL * k_blocks * F8_BK));
+  if (a_rows <= b_rows) return (int)std::min<long long>(num_m, g);
+  return -(int)std::min<long long>(num_n, g);
+}
+
+template <int EPI, bool A_MN, bool B_MN, bool VEC>
+coda_status launch_gemm8(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to1, const CUtensorMap& to2,
+                         Gemm8Params p, cudaStream_t s) {
+  static std::atomic<int> clusters_of[kMaxDevices];  // 0: not set up on this device yet
+  int dev = 0;
+  coda_status st = current_device(dev);
+  if (st != CODA_OK) return st;
+  auto kern = gemm_fp8_kernel<EPI, A_MN, B_MN, VEC>;
+  int clusters = clusters_of[dev].load();
+  if (clusters == 0) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F8_SMEM_BYTES) != cudaSuccess)
+      return CODA_ERR_CUDA;
+    clusters = g_dev[dev].num_sms / 2;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2 * clusters, 1, 1);
+    cfg.blockDim = dim3(F8_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = F8_SMEM_BYTES;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0) clusters = std::min(clusters, n);
+    clusters_of[dev].store(clusters);
+  }
+  p.wait_limit_ns = g_wait_limit_ns.load();
+  p.kernel_id = 0x40 + (uint32_t)(EPI * 8 + (A_MN ? 4 : 0) + (B_MN ? 2 : 0) + (VEC ? 1 : 0));
+  const long long tiles = (long long)p.num_m_tiles * p.num_n_tiles;
+  const int units = (int)std::min<long long>(tiles, clusters);
+  g_launch_tag = EPI == F8_EPI_SWIGLU ? CODA_KERNEL_GEMM_SWIGLU_FP8 : CODA_KERNEL_GEMM_FP8;
+  const cudaError_t e =
+      launch_ex(kern, dim3(2 * units), dim3(F8_THREADS), F8_SMEM_BYTES, s, 2, ta, tb, to1, to2, p);
+  g_launch_tag = -1;
+  return e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess ? CODA_OK : CODA_ERR_CUDA;
+}
+
+template <int EPI, bool VEC>
+coda_status launch_gemm8_majors(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to, bool a_mn,
+                                bool b_mn, const Gemm8Params& p, cudaStream_t s) {
+  if (!a_mn && !b_mn) return launch_gemm8<EPI, false, false, VEC>(ta, tb, to, to, p, s);
+  if (!a_mn && b_mn) return launch_gemm8<EPI, false, true, VEC>(ta, tb, to, to, p, s);
+  if (a_mn && b_mn) return launch_gemm8<EPI, true, true, VEC>(ta, tb, to, to, p, s);
+  return launch_gemm8<EPI, true, false, VEC>(ta, tb, to, to, p, s);
+}
+
+inline bool known_format(int f) { return f == CODA_FP8_E4M3 || f == CODA_FP8_E5M2; }
+inline bool tiles_fit(long long a, long long b) { return a * b <= 0x7FFFFFFFLL; }
+
+// One launch of a light pass under its timing-hook id.
+template <typename... KArgs, typename P>
+coda_status launch_pass(int tag, void (*kern)(KArgs...), int grid, int block, void* stream, const P& p) {
+  g_launch_tag = tag;
+  const cudaError_t e = launch_ex(kern, dim3(grid), dim3(block), 0, static_cast<cudaStream_t>(stream), 1, p);
+  g_launch_tag = -1;
+  return launch_status(e);
+}
+
+template <int FMT>
+coda_status quant8(const QuantParams& p, bool rows, bool cols, bool vec, int grid, void* stream) {
+  const int tag = CODA_KERNEL_QUANT_FP8;
+  if (vec) {
+    if (rows && cols) return launch_pass(tag, quant_fp8_kernel<FMT, true, true, false, true>, grid, kQuantThreads, stream, p);
+    if (rows) return launch_pass(tag, quant_fp8_kernel<FMT, true, false, false, true>, grid, kQuantThreads, stream, p);
+    return launch_pass(tag, quant_fp8_kernel<FMT, false, true, false, true>, grid, kQuantThreads, stream, p);
+  }
+  if (rows && cols) return launch_pass(tag, quant_fp8_kernel<FMT, true, true, false, false>, grid, kQuantThreads, stream, p);
+  if (rows) return launch_pass(tag, quant_fp8_kernel<FMT, true, false, false, false>, grid, kQuantThreads, stream, p);
+  return launch_pass(tag, quant_fp8_kernel<FMT, false, true, false, false>, grid, kQuantThreads, stream, p);
+}
+
+template <int T, int CH>
+coda_status rms8_fwd(const RmsParams& p, void* stream) {
+  return launch_pass(CODA_KERNEL_RMSNORM_FP8_FWD, rmsnorm_fp8_fwd_kernel<T, CH>, p.M, T, stream, p);
+}
+
+// Widest row the norms hold in registers.
+constexpr int kRms8MaxD = 1024 * 4 * 8;
+
+// CTAs of the norm's backward: each keeps its share of dg in registers and
+// writes one partial row, so a few per SM.
+constexpr int kRms8BwdCtas = 592;
+int rms8_bwd_ctas(int M) { return std::min(M, kRms8BwdCtas); }
+
+template <int T, int CH>
+coda_status rms8_bwd(const RmsBwdParams& p, void* stream) {
+  return launch_pass(CODA_KERNEL_RMSNORM_FP8_BWD, rmsnorm_fp8_bwd_kernel<T, CH>, rms8_bwd_ctas(p.M), T, stream, p);
+}
+
+}  // namespace
+}  // namespace coda
+
+extern "C" {
+
+// ------------------------------------------------------------------ quantiser
+
+coda_status coda_quant_fp8(const void* X, const float* rowvec_or_null, const void* colvec_or_null, void* Qr_or_null,
+                           float* Sr_or_null, void* Qc_or_null, float* Sc_or_null, int R, int C, int format,
+                           void* stream) {
+  const bool rows = Qr_or_null != nullptr || Sr_or_null != nullptr;
+  const bool cols = Qc_or_null != nullptr || Sc_or_null != nullptr;
+  if (R < 0 || C < 1 || !known_format(format)) return CODA_ERR_INVALID_ARG;
+  if (C % 16 != 0 || !tiles_fit(cdiv(R, kScaleBlock), cdiv(C, kScaleBlock))) return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (R == 0) return CODA_OK;
+  if (!X || (!rows && !cols)) return CODA_ERR_INVALID_ARG;
+  if (rows && (!Qr_or_null || !Sr_or_null)) return CODA_ERR_INVALID_ARG;
+  if (cols && (!Qc_or_null || !Sc_or_null)) return CODA_ERR_INVALID_ARG;
+  const void* ptrs[] = {X, rowvec_or_null, colvec_or_null, Qr_or_null, Sr_or_null, Qc_or_null, Sc_or_null};
+  for (const void* q : ptrs)
+    if (q && !aligned16(q)) return CODA_ERR_MISALIGNED;
+  int dev;
+  CODA_TRY(current_device(dev));
+  QuantParams p;
+  p.x = cbf(X);
+  p.rowvec = rowvec_or_null;
+  p.colvec = cbf(colvec_or_null);
+  p.qr = static_cast<uint8_t*>(Qr_or_null);
+  p.sr = Sr_or_null;
+  p.qc = static_cast<uint8_t*>(Qc_or_null);
+  p.sc = Sc_or_null;
+  p.R = R;
+  p.C = C;
+  p.tiles_c = cdiv(C, kScaleBlock);
+  const int grid = cdiv(R, kScaleBlock) * p.tiles_c;
+  const bool vec = rowvec_or_null != nullptr || colvec_or_null != nullptr;
+  return format == CODA_FP8_E4M3 ? quant8<FP8_E4M3>(p, rows, cols, vec, grid, stream)
+                                 : quant8<FP8_E5M2>(p, rows, cols, vec, grid, stream);
+}
+
+coda_status coda_quant_fp8_blocks(const void* W, void* Q, float* S, int R, int C, int format, void* stream) {
+  if (R < 0 || C < 1 || !known_format(format)) return CODA_ERR_INVALID_ARG;
+  if (C % 16 != 0 || !tiles_fit(cdiv(R, kScaleBlock), cdiv(C, kScaleBlock))) return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (R == 0) return CODA_OK;
+  if (!W || !Q || !S) return CODA_ERR_INVALID_ARG;
+  if (!aligned16(W) || !aligned16(Q) || !aligned16(S)) return CODA_ERR_MISALIGNED;
+  int dev;
+  CODA_TRY(current_device(dev));
+  QuantParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.x = cbf(W);
+  p.qc = static_cast<uint8_t*>(Q);
+  p.sc = S;
+  p.R = R;
+  p.C = C;
+  p.tiles_c = cdiv(C, kScaleBlock);
+  const int grid = cdiv(R, kScaleBlock) * p.tiles_c;
+  if (format == CODA_FP8_E4M3)
+    return launch_pass(CODA_KERNEL_QUANT_FP8, quant_fp8_kernel<FP8_E4M3, false, false, true, false>, grid,
+                       kQuantThreads, stream, p);
+  return launch_pass(CODA_KERNEL_QUANT_FP8, quant_fp8_kernel<FP8_E5M2, false, false, true, false>, grid,
+                     kQuantThreads, stream, p);
+}
+
+// ------------------------------------------------------------------ GEMM
+
+coda_status coda_gemm_fp8(const void* A, const float* SA, const void* B, const float* SB, void* C, int M, int N, int K,
+                          int a_mn_major, int b_mn_major, int a_format, int b_format, int b_blocks, int c_fp32,
+                          int accumulate, void* ws, size_t ws_bytes, void* stream) {
+  if (M < 0 || N < 0 || K < 0 || !known_format(a_format) || !known_format(b_format)) return CODA_ERR_INVALID_ARG;
+  if (accumulate && !c_fp32) return CODA_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return CODA_OK;  // empty output
+  if (N % 16 != 0 || (a_mn_major ? M : K) % 16 != 0 || (!b_mn_major && K % 16 != 0)) return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (!tiles_fit(cdiv(M, 256), cdiv(N, 256))) return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (K == 0) {  // empty sums
+    if (!C) return CODA_ERR_INVALID_ARG;
+    return accumulate ? CODA_OK : zero_fill({{C, (size_t)M * N * (c_fp32 ? 4 : 2)}}, stream);
+  }
+  if (!A || !SA || !B || !SB || !C || !ws) return CODA_ERR_INVALID_ARG;
+  const void* ptrs[] = {A, SA, B, SB, C, ws};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return CODA_ERR_MISALIGNED;
+  if (ws_bytes < coda_gemm_workspace_bytes()) return CODA_ERR_WORKSPACE_TOO_SMALL;
+  int dev;
+  CODA_TRY(current_device(dev));
+  const bool a_mn = a_mn_major != 0, b_mn = b_mn_major != 0;
+  CUtensorMap ta, tb, to;
+  if (!operand8_map_a(&ta, A, M, K, a_mn) || !operand8_map_b(&tb, B, N, K, b_mn)) return CODA_ERR_CUDA;
+  if (!(c_fp32 ? make_tmap8(&to, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, C, M, N, 16, 32, CU_TENSOR_MAP_SWIZZLE_64B)
+               : make_tmap8(&to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, C, M, N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)))
+    return CODA_ERR_CUDA;
+  Gemm8Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.num_m_tiles = cdiv(M, 256);
+  p.num_n_tiles = cdiv(N, 256);
+  p.k_blocks = cdiv(K, F8_BK);
+  p.group_m = pick_group8(M, N, p.num_m_tiles, p.num_n_tiles, p.k_blocks, num_sms() / 2);
+  p.sa = SA;
+  p.sb = SB;
+  // Block scales of the stored matrix: [N / 128, K / 128], or [K / 128, N / 128] when k is the row.
+  p.sb_n = b_mn ? 1 : p.k_blocks;
+  p.sb_k = b_mn ? cdiv(N, kScaleBlock) : 1;
+  p.add = accumulate;
+  p.idesc = make_idesc_f8(256, 128, a_format, b_format, a_mn, b_mn);
+  p.status = static_cast<uint32_t*>(ws);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (c_fp32)
+    return b_blocks ? launch_gemm8_majors<F8_EPI_F32, false>(ta, tb, to, a_mn, b_mn, p, s)
+                    : launch_gemm8_majors<F8_EPI_F32, true>(ta, tb, to, a_mn, b_mn, p, s);
+  return b_blocks ? launch_gemm8_majors<F8_EPI_BF16, false>(ta, tb, to, a_mn, b_mn, p, s)
+                  : launch_gemm8_majors<F8_EPI_BF16, true>(ta, tb, to, a_mn, b_mn, p, s);
+}
+
+coda_status coda_gemm_swiglu_fp8(const void* A, const float* SA, const void* Wgu, const float* SW, void* Y, float* SY,
+                                 void* AB_or_null, float* SAB_or_null, int M, int K, int F, void* ws, size_t ws_bytes,
+                                 void* stream) {
+  if (M < 0 || K < 1 || F < 1) return CODA_ERR_INVALID_ARG;
+  if (K % 16 != 0 || F % kScaleBlock != 0 || F > 0x3FFFFFFF || !tiles_fit(cdiv(M, 256), F / kScaleBlock))
+    return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return CODA_OK;
+  if (!A || !SA || !Wgu || !SW || !Y || !SY || !ws) return CODA_ERR_INVALID_ARG;
+  if ((AB_or_null == nullptr) != (SAB_or_null == nullptr)) return CODA_ERR_INVALID_ARG;
+  const void* ptrs[] = {A, SA, Wgu, SW, Y, SY, AB_or_null, SAB_or_null, ws};
+  for (const void* q : ptrs)
+    if (q && !aligned16(q)) return CODA_ERR_MISALIGNED;
+  if (ws_bytes < coda_gemm_workspace_bytes()) return CODA_ERR_WORKSPACE_TOO_SMALL;
+  int dev;
+  CODA_TRY(current_device(dev));
+  CUtensorMap ta, tb, to1, to2;
+  if (!operand8_map_a(&ta, A, M, K, false) || !operand8_map_b(&tb, Wgu, 2LL * F, K, false)) return CODA_ERR_CUDA;
+  if (!make_tmap8(&to1, kU8, 1, Y, M, F, 64, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return CODA_ERR_CUDA;
+  to2 = to1;
+  if (AB_or_null && !make_tmap8(&to2, kU8, 1, AB_or_null, M, 2LL * F, 64, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    return CODA_ERR_CUDA;
+  Gemm8Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.M = M;
+  p.N = F;
+  p.K = K;
+  p.num_m_tiles = cdiv(M, 256);
+  p.num_n_tiles = F / kScaleBlock;
+  p.k_blocks = cdiv(K, F8_BK);
+  p.group_m = pick_group8(M, 2LL * F, p.num_m_tiles, p.num_n_tiles, p.k_blocks, num_sms() / 2);
+  p.sa = SA;
+  p.sb = SW;
+  p.sb_n = p.k_blocks;
+  p.sb_k = 1;
+  p.split = F;
+  p.save_ab = AB_or_null != nullptr;
+  p.sy = SY;
+  p.sab = SAB_or_null;
+  p.idesc = make_idesc_f8(256, 128, FP8_E4M3, FP8_E4M3, false, false);
+  p.status = static_cast<uint32_t*>(ws);
+  return launch_gemm8<F8_EPI_SWIGLU, false, false, false>(ta, tb, to1, to2, p, static_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------------------------ SwiGLU backward
+
+coda_status coda_swiglu_fp8_bwd(const void* dY, const void* AB, const float* SAB, void* dA, float* SdA,
+                                void* dAc_or_null, float* SdAc_or_null, void* Yc_or_null, float* SYc_or_null, int M,
+                                int F, int format, void* stream) {
+  if (M < 0 || F < 1 || !known_format(format)) return CODA_ERR_INVALID_ARG;
+  if (F % kScaleBlock != 0 || F > 0x3FFFFFFF || !tiles_fit(cdiv(M, kScaleBlock), F / kScaleBlock))
+    return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return CODA_OK;
+  if (!dY || !AB || !SAB || !dA || !SdA) return CODA_ERR_INVALID_ARG;
+  const void* cols[] = {dAc_or_null, SdAc_or_null, Yc_or_null, SYc_or_null};
+  int given = 0;
+  for (const void* q : cols) given += q != nullptr;
+  if (given != 0 && given != 4) return CODA_ERR_INVALID_ARG;
+  const void* ptrs[] = {dY, AB, SAB, dA, SdA, dAc_or_null, SdAc_or_null, Yc_or_null, SYc_or_null};
+  for (const void* q : ptrs)
+    if (q && !aligned16(q)) return CODA_ERR_MISALIGNED;
+  int dev;
+  CODA_TRY(current_device(dev));
+  SwigluBwd8Params p;
+  p.dy = cbf(dY);
+  p.ab = static_cast<const uint8_t*>(AB);
+  p.sab = SAB;
+  p.da = static_cast<uint8_t*>(dA);
+  p.sda = SdA;
+  p.dac = static_cast<uint8_t*>(dAc_or_null);
+  p.sdac = SdAc_or_null;
+  p.yc = static_cast<uint8_t*>(Yc_or_null);
+  p.syc = SYc_or_null;
+  p.M = M;
+  p.F = F;
+  const int grid = cdiv(M, kScaleBlock) * (F / kScaleBlock);
+  const int tag = CODA_KERNEL_SWIGLU_FP8_BWD;
+  if (format == CODA_FP8_E4M3)
+    return given ? launch_pass(tag, swiglu_fp8_bwd_kernel<FP8_E4M3, true>, grid, kSwBwdThreads, stream, p)
+                 : launch_pass(tag, swiglu_fp8_bwd_kernel<FP8_E4M3, false>, grid, kSwBwdThreads, stream, p);
+  return given ? launch_pass(tag, swiglu_fp8_bwd_kernel<FP8_E5M2, true>, grid, kSwBwdThreads, stream, p)
+               : launch_pass(tag, swiglu_fp8_bwd_kernel<FP8_E5M2, false>, grid, kSwBwdThreads, stream, p);
+}
+
+// ------------------------------------------------------------------ RMSNorm
+
+coda_status coda_rmsnorm_fp8_fwd(const void* X, const void* R_or_null, const void* g, void* H_or_null, float* r,
+                                 void* Q, float* S, int M, int d, float eps, void* stream) {
+  if (M < 0 || d < 1 || !(eps > 0.f)) return CODA_ERR_INVALID_ARG;
+  if (d % 16 != 0 || d > kRms8MaxD) return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return CODA_OK;
+  if (!X || !g || !r || !Q || !S || (R_or_null == nullptr) != (H_or_null == nullptr)) return CODA_ERR_INVALID_ARG;
+  const void* ptrs[] = {X, R_or_null, g, H_or_null, r, Q, S};
+  for (const void* q : ptrs)
+    if (q && !aligned16(q)) return CODA_ERR_MISALIGNED;
+  int dev;
+  CODA_TRY(current_device(dev));
+  RmsParams p;
+  p.x = cbf(X);
+  p.res = cbf(R_or_null);
+  p.g = cbf(g);
+  p.h = bf(H_or_null);
+  p.r = r;
+  p.q = static_cast<uint8_t*>(Q);
+  p.s = S;
+  p.M = M;
+  p.d = d;
+  p.inv_d = 1.0f / (float)d;
+  p.eps = eps;
+  const int chunks = d / 8;
+  if (chunks <= 128) return rms8_fwd<128, 1>(p, stream);
+  if (chunks <= 256) return rms8_fwd<256, 1>(p, stream);
+  if (chunks <= 512) return rms8_fwd<256, 2>(p, stream);
+  if (chunks <= 1024) return rms8_fwd<256, 4>(p, stream);
+  if (chunks <= 2048) return rms8_fwd<512, 4>(p, stream);
+  return rms8_fwd<1024, 4>(p, stream);
+}
+
+size_t coda_rmsnorm_fp8_bwd_workspace_bytes(int M, int d) {
+  if (M < 1 || d < 1) return kStatusBytes;
+  return kStatusBytes + (size_t)rms8_bwd_ctas(M) * d * 4;
+}
+
+coda_status coda_rmsnorm_fp8_bwd(const void* dN, const void* H, const float* r, const void* g,
+                                 const void* dH_in_or_null, void* dH, float* dg, int M, int d, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  if (M < 0 || d < 1) return CODA_ERR_INVALID_ARG;
+  if (d % 16 != 0 || d > kRms8MaxD) return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return zero_fill({{dg, (size_t)d * 4}}, stream);
+  if (!dN || !H || !r || !g || !dH || !dg || !ws) return CODA_ERR_INVALID_ARG;
+  const void* ptrs[] = {dN, H, r, g, dH_in_or_null, dH, dg, ws};
+  for (const void* q : ptrs)
+    if (q && !aligned16(q)) return CODA_ERR_MISALIGNED;
+  if (ws_bytes < coda_rmsnorm_fp8_bwd_workspace_bytes(M, d)) return CODA_ERR_WORKSPACE_TOO_SMALL;
+  int dev;
+  CODA_TRY(current_device(dev));
+  RmsBwdParams p;
+  p.dn = cbf(dN);
+  p.h = cbf(H);
+  p.r = r;
+  p.g = cbf(g);
+  p.dh_in = cbf(dH_in_or_null);
+  p.dh = bf(dH);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes);
+  p.M = M;
+  p.d = d;
+  p.inv_d = 1.0f / (float)d;
+  const int chunks = d / 8;
+  coda_status st;
+  if (chunks <= 128) st = rms8_bwd<128, 1>(p, stream);
+  else if (chunks <= 256) st = rms8_bwd<256, 1>(p, stream);
+  else if (chunks <= 512) st = rms8_bwd<256, 2>(p, stream);
+  else if (chunks <= 1024) st = rms8_bwd<512, 2>(p, stream);
+  else if (chunks <= 2048) st = rms8_bwd<512, 4>(p, stream);
+  else st = rms8_bwd<1024, 4>(p, stream);
+  if (st != CODA_OK) return st;
+  return launch_status(launch_ex(col_reduce_kernel, dim3(cdiv(d, 32)), dim3(COLRED_THREADS), 0,
+                                 static_cast<cudaStream_t>(stream), 1, (const float*)p.part, rms8_bwd_ctas(M), d, dg));
+}
+
+}  // extern "C"

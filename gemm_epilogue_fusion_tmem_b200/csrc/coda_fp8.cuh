@@ -1,0 +1,531 @@
+// The 8-bit passes around the 8-bit GEMMs: quantisation of an activation, a
+// gradient or a weight; RMSNorm with the residual and an 8-bit output, and its
+// backward; the SwiGLU backward from an 8-bit checkpoint of [a | b].
+//
+// Numbers: a block of up to 128 values shares one fp32 scale.  With amax the
+// largest magnitude in the block and c = max(amax, 2^-100),
+//   S = c / fmax,   q = round_to_8_bits(x * (fmax / c)),   x ~ q * S,
+// fmax = 448 (e4m3) or 57344 (e5m2): the block's largest value lands on the
+// type's largest.  The floor 2^-100 keeps fmax / c finite, so an all-zero
+// block has q = 0 and a positive scale.  NaNs are left out of amax and stay
+// NaN in q; a block that holds an infinity has S = inf and comes back as NaN.
+//
+// Blocks of a stored matrix [R, C]: rows (1 x 128, S [ceil(C/128), R]),
+// columns (128 x 1, S [ceil(R/128), C]) or 128 x 128 (S [ceil(R/128),
+// ceil(C/128)]).  Row and column scales keep the blocked axis first: a product
+// reduces over that axis, and its tile reads one contiguous line of scales per
+// 128 of the reduction.
+#pragma once
+
+#include "coda_ptx.cuh"
+
+namespace coda {
+
+enum Fp8 : int { FP8_E4M3 = 0, FP8_E5M2 = 1 };
+
+template <int FMT>
+__host__ __device__ constexpr float fp8_max() {
+  return FMT == FP8_E4M3 ? 448.f : 57344.f;
+}
+constexpr float kFp8Tiny = 7.888609052210118e-31f;  // 2^-100
+
+// Scale of a block and the factor its values are multiplied by.
+template <int FMT>
+__device__ __forceinline__ float fp8_scale(float amax) {
+  return fmaxf(amax, kFp8Tiny) * (1.0f / fp8_max<FMT>());
+}
+template <int FMT>
+__device__ __forceinline__ float fp8_factor(float amax) {
+  return __fdiv_rn(fp8_max<FMT>(), fmaxf(amax, kFp8Tiny));
+}
+
+// Two floats to two 8-bit values (lo in the low byte), nearest even, saturating.
+template <int FMT>
+__device__ __forceinline__ uint32_t fp8_pack2(float lo, float hi) {
+  uint16_t r;
+  if constexpr (FMT == FP8_E4M3)
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d) {
+  return fp8_pack2<FMT>(a, b) | (fp8_pack2<FMT>(c, d) << 16);
+}
+template <int FMT>
+__device__ __forceinline__ uint2 fp8_pack8(const float* f, float factor) {
+  return make_uint2(fp8_pack4<FMT>(f[0] * factor, f[1] * factor, f[2] * factor, f[3] * factor),
+                    fp8_pack4<FMT>(f[4] * factor, f[5] * factor, f[6] * factor, f[7] * factor));
+}
+
+// Four e4m3 values of a word to floats (exact: e4m3 is a subset of fp16).
+__device__ __forceinline__ void e4m3_unpack4(uint32_t w, float* f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w >> (16 * i))));
+    const float2 v = __half22float2(*reinterpret_cast<__half2*>(&h));
+    f[2 * i] = v.x;
+    f[2 * i + 1] = v.y;
+  }
+}
+
+__device__ __forceinline__ uint2 ldg_nc_v2(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void stg_v2(void* p, const uint2& v) {
+  asm volatile("st.global.v2.u32 [%0], {%1,%2};" ::"l"(p), "r"(v.x), "r"(v.y) : "memory");
+}
+
+// Largest of the 16 lanes that hold one row's 128 columns.
+__device__ __forceinline__ float max16(float v) {
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// ------------------------------------------------------------------ quantiser
+
+// One CTA per 128 x 128 tile, read once: a thread holds 8 columns of 8 rows
+// (16 threads to a row), so row maxima are 4 shuffles and column maxima one
+// shuffle and a pass over the 8 warps' maxima in shared memory; the values are
+// then rounded once per requested form.  With VEC the matrix is
+// X diag-scaled by rowvec (fp32, rows) and colvec (bf16, columns), which gives
+// the column form of RMSNorm's output from H, r and g without storing it.
+constexpr int kQuantThreads = 256;
+constexpr int kQuantRows = 128 * 16 / kQuantThreads;  // rows per thread
+
+struct QuantParams {
+  const __nv_bfloat16* x;
+  const float* rowvec;
+  const __nv_bfloat16* colvec;
+  uint8_t *qr, *qc;
+  float *sr, *sc;
+  int R, C, tiles_c;
+};
+
+template <int FMT, bool ROWS, bool COLS, bool BLOCKS, bool VEC>
+__global__ void __launch_bounds__(kQuantThreads) quant_fp8_kernel(const QuantParams p) {
+  __shared__ float smax[kQuantThreads / 32][128];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int tr = blockIdx.x / p.tiles_c, tc = blockIdx.x - tr * p.tiles_c;
+  const int c0 = tc * 128 + (lane % 16) * 8;
+  const int r0 = tr * 128 + warp * 2 + lane / 16;  // then + 16 per step
+  const bool cv = c0 < p.C;
+  uint4 x[kQuantRows];
+#pragma unroll
+  for (int i = 0; i < kQuantRows; ++i) {
+    const int row = r0 + 16 * i;
+    x[i] = (cv && row < p.R) ? ldg_nc_v4(p.x + (size_t)row * p.C + c0) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  float cvec[8], rvec[kQuantRows];
+  if constexpr (VEC) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cvec[j] = 1.f;
+    if (p.colvec != nullptr && cv) unpack8(ldg_nc_v4_l1(p.colvec + c0), cvec);
+#pragma unroll
+    for (int i = 0; i < kQuantRows; ++i) {
+      const int row = r0 + 16 * i;
+      rvec[i] = (p.rowvec != nullptr && row < p.R) ? p.rowvec[row] : 1.f;
+    }
+  }
+  auto values = [&](int i, float* f) {
+    unpack8(x[i], f);
+    if constexpr (VEC) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = f[j] * rvec[i] * cvec[j];
+    }
+  };
+  float cmax[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) cmax[j] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kQuantRows; ++i) {
+    float f[8];
+    values(i, f);
+    float rmax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      rmax = fmaxf(rmax, fabsf(f[j]));
+      cmax[j] = fmaxf(cmax[j], fabsf(f[j]));
+    }
+    if constexpr (ROWS) {
+      rmax = max16(rmax);
+      const int row = r0 + 16 * i;
+      if (row < p.R) {
+        if (cv) stg_v2(p.qr + (size_t)row * p.C + c0, fp8_pack8<FMT>(f, fp8_factor<FMT>(rmax)));
+        if (lane % 16 == 0) p.sr[(size_t)tc * p.R + row] = fp8_scale<FMT>(rmax);
+      }
+    }
+  }
+  if constexpr (COLS || BLOCKS) {
+    if constexpr (BLOCKS) {
+      float m = cmax[0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) m = fmaxf(m, cmax[j]);
+      m = max16(m);
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+      if (lane == 0) smax[warp][0] = m;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kQuantThreads / 32; ++w) m = fmaxf(m, smax[w][0]);
+      if (threadIdx.x == 0) p.sc[(size_t)tr * p.tiles_c + tc] = fp8_scale<FMT>(m);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) cmax[j] = m;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) cmax[j] = fmaxf(cmax[j], __shfl_xor_sync(0xffffffffu, cmax[j], 16));
+      if (lane < 16) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) smax[warp][lane * 8 + j] = cmax[j];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kQuantThreads / 32; ++w) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) cmax[j] = fmaxf(cmax[j], smax[w][(lane % 16) * 8 + j]);
+      }
+      if (warp == 0 && lane < 16 && cv) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p.sc[(size_t)tr * p.C + c0 + j] = fp8_scale<FMT>(cmax[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cmax[j] = fp8_factor<FMT>(cmax[j]);
+#pragma unroll
+    for (int i = 0; i < kQuantRows; ++i) {
+      const int row = r0 + 16 * i;
+      float f[8];
+      values(i, f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] *= cmax[j];
+      if (cv && row < p.R) stg_v2(p.qc + (size_t)row * p.C + c0, fp8_pack8<FMT>(f, 1.f));
+    }
+  }
+}
+
+// ------------------------------------------------------------------ RMSNorm
+
+// Sum over the block's THREADS threads, in every thread.  `scratch` holds
+// THREADS / 32 floats and is free again after the next block-wide barrier.
+template <int THREADS>
+__device__ __forceinline__ float block_sum_all(float v, float* scratch) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (THREADS == 32) return v;
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x / 32] = v;
+  __syncthreads();
+  float t = (threadIdx.x & 31) < THREADS / 32 ? scratch[threadIdx.x & 31] : 0.f;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return t;
+}
+
+struct RmsParams {
+  const __nv_bfloat16 *x, *res, *g;
+  __nv_bfloat16* h;
+  float* r;
+  uint8_t* q;
+  float* s;
+  int M, d;
+  float inv_d, eps;
+};
+
+// H = bf16(X + R); r = rsqrt(mean_j H_j^2 + eps) from the stored H;
+// (Q, S) = row blocks of H r g.  One CTA per row, the row in registers (CH
+// chunks of 8 columns per thread), so X and R are read once and nothing is
+// read back; 16 neighbouring threads hold one scale block.
+template <int THREADS, int CH>
+__global__ void __launch_bounds__(THREADS) rmsnorm_fp8_fwd_kernel(const RmsParams p) {
+  __shared__ float scratch[32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int row = blockIdx.x;
+  const size_t base = (size_t)row * p.d;
+  uint4 hq[CH];
+  float ss = 0.f;
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int c = (k * THREADS + threadIdx.x) * 8;
+    hq[k] = c < p.d ? ldg_nc_v4(p.x + base + c) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (p.res != nullptr) {
+    uint4 rq[CH];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int c = (k * THREADS + threadIdx.x) * 8;
+      rq[k] = c < p.d ? ldg_nc_v4(p.res + base + c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int c = (k * THREADS + threadIdx.x) * 8;
+      float a[8], b[8];
+      unpack8(hq[k], a);
+      unpack8(rq[k], b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] += b[i];
+      hq[k] = pack8(a);
+      if (c < p.d) stg_v4(p.h + base + c, hq[k]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    float a[8];
+    unpack8(hq[k], a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], ss);
+  }
+  const float r = rsqrtf(fmaf(block_sum_all<THREADS>(ss, scratch), p.inv_d, p.eps));
+  if (threadIdx.x == 0) p.r[row] = r;
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int c = (k * THREADS + threadIdx.x) * 8;
+    const bool v = c < p.d;
+    float a[8], g[8];
+    unpack8(hq[k], a);
+    unpack8(v ? ldg_nc_v4_l1(p.g + c) : make_uint4(0u, 0u, 0u, 0u), g);
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a[i] = a[i] * r * g[i];
+      m = fmaxf(m, fabsf(a[i]));
+    }
+    m = max16(m);
+    if (v) {
+      stg_v2(p.q + base + c, fp8_pack8<FP8_E4M3>(a, fp8_factor<FP8_E4M3>(m)));
+      if (threadIdx.x % 16 == 0) p.s[(size_t)(c / 128) * p.M + row] = fp8_scale<FP8_E4M3>(m);
+    }
+  }
+}
+
+struct RmsBwdParams {
+  const __nv_bfloat16 *dn, *h, *g, *dh_in;
+  const float* r;
+  __nv_bfloat16* dh;
+  float* part;  // [gridDim.x][d] partial sums of dg
+  int M, d;
+  float inv_d;
+};
+
+// u = dN g;  dH = r u - H r^3 mean_j(u_j H_j) (+ dH_in);  dg partials: each CTA
+// takes every gridDim.x-th row and keeps sum_i dN_i H_i r_i of its columns in
+// registers, so one pass reads everything once; col_reduce_kernel adds the
+// CTAs' partials in a fixed order.
+template <int THREADS, int CH>
+__global__ void __launch_bounds__(THREADS) rmsnorm_fp8_bwd_kernel(const RmsBwdParams p) {
+  __shared__ float scratch[2][32];
+  griddep_wait();
+  griddep_launch_dependents();
+  float dg[CH][8];
+#pragma unroll
+  for (int k = 0; k < CH; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dg[k][i] = 0.f;
+  int parity = 0;
+  for (int row = blockIdx.x; row < p.M; row += gridDim.x, parity ^= 1) {
+    const size_t base = (size_t)row * p.d;
+    const float r = p.r[row];
+    uint4 nq[CH], hq[CH];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int c = (k * THREADS + threadIdx.x) * 8;
+      nq[k] = c < p.d ? ldg_nc_v4(p.dn + base + c) : make_uint4(0u, 0u, 0u, 0u);
+      hq[k] = c < p.d ? ldg_nc_v4(p.h + base + c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int c = (k * THREADS + threadIdx.x) * 8;
+      float n[8], h[8], g[8];
+      unpack8(nq[k], n);
+      unpack8(hq[k], h);
+      unpack8(c < p.d ? ldg_nc_v4_l1(p.g + c) : make_uint4(0u, 0u, 0u, 0u), g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float nh = n[i] * h[i];
+        s = fmaf(nh, g[i], s);
+        dg[k][i] = fmaf(nh, r, dg[k][i]);
+      }
+    }
+    // Two scratch rows in turn: a thread may still read one while another starts the next row.
+    const float coef = block_sum_all<THREADS>(s, scratch[parity]) * p.inv_d * r * r * r;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int c = (k * THREADS + threadIdx.x) * 8;
+      if (c >= p.d) continue;
+      float n[8], h[8], g[8];
+      unpack8(nq[k], n);
+      unpack8(hq[k], h);
+      unpack8(ldg_nc_v4_l1(p.g + c), g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n[i] = fmaf(n[i] * g[i], r, -coef * h[i]);
+      if (p.dh_in != nullptr) {
+        unpack8(ldg_nc_v4(p.dh_in + base + c), g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n[i] += g[i];
+      }
+      stg_v4(p.dh + base + c, pack8(n));
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int c = (k * THREADS + threadIdx.x) * 8;
+    if (c >= p.d) continue;
+    float* o = p.part + (size_t)blockIdx.x * p.d + c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = dg[k][i];
+  }
+}
+
+// ------------------------------------------------------------------ SwiGLU backward from the 8-bit checkpoint
+
+// With s = sigmoid(a): da = dY b s (1 + a (1 - s)), db = dY a s, y = a s b.
+// One CTA per 128 tokens x 128 columns: dY (bf16) and the saved a, b (e4m3 and
+// one scale per row and 128 columns) are read once and held packed in
+// registers; the gradients are formed twice, once for the row and column
+// maxima and once to be rounded, which costs less than keeping 96 floats per
+// thread.  Outputs: dA = [da | db] in row blocks (operand of dgrad) and, with
+// COLS, dA and y in column blocks (operands of the two weight gradients).
+constexpr int kSwBwdThreads = 512;
+constexpr int kSwBwdRows = 128 * 16 / kSwBwdThreads;  // rows per thread
+
+struct SwigluBwd8Params {
+  const __nv_bfloat16* dy;
+  const uint8_t* ab;
+  const float* sab;
+  uint8_t *da, *dac, *yc;
+  float *sda, *sdac, *syc;
+  int M, F;
+};
+
+template <int FMT, bool COLS>
+__global__ void __launch_bounds__(kSwBwdThreads) swiglu_fp8_bwd_kernel(const SwigluBwd8Params p) {
+  __shared__ float smax[COLS ? kSwBwdThreads / 32 : 1][3][128];
+  __shared__ float sfac[3][128];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int fb = p.F / 128;
+  const int tr = blockIdx.x / fb, tc = blockIdx.x - tr * fb;
+  const int c0 = tc * 128 + (lane % 16) * 8;
+  const int r0 = tr * 128 + warp * 2 + lane / 16;  // then + 2 * warps per step
+  constexpr int STEP = kSwBwdThreads / 16;
+  uint4 dyq[kSwBwdRows];
+  uint2 aq[kSwBwdRows], bq[kSwBwdRows];
+  float as[kSwBwdRows], bs[kSwBwdRows];
+#pragma unroll
+  for (int i = 0; i < kSwBwdRows; ++i) {
+    const int row = r0 + STEP * i;
+    dyq[i] = make_uint4(0u, 0u, 0u, 0u);
+    aq[i] = bq[i] = make_uint2(0u, 0u);
+    as[i] = bs[i] = 0.f;
+    if (row < p.M) {
+      dyq[i] = ldg_nc_v4(p.dy + (size_t)row * p.F + c0);
+      aq[i] = ldg_nc_v2(p.ab + (size_t)row * 2 * p.F + c0);
+      bq[i] = ldg_nc_v2(p.ab + (size_t)row * 2 * p.F + p.F + c0);
+      as[i] = p.sab[(size_t)tc * p.M + row];
+      bs[i] = p.sab[(size_t)(fb + tc) * p.M + row];
+    }
+  }
+  // da, db, y of row step i.
+  auto grads = [&](int i, float* da, float* db, float* y) {
+    float dy[8], a[8], b[8];
+    unpack8(dyq[i], dy);
+    e4m3_unpack4(aq[i].x, a);
+    e4m3_unpack4(aq[i].y, a + 4);
+    e4m3_unpack4(bq[i].x, b);
+    e4m3_unpack4(bq[i].y, b + 4);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float av = a[j] * as[i], bv = b[j] * bs[i];
+      const float s = sigmoid_f(av);
+      const float as_ = av * s;
+      da[j] = dy[j] * bv * fmaf(as_, 1.f - s, s);
+      db[j] = dy[j] * as_;
+      y[j] = as_ * bv;
+    }
+  };
+  float cmax[3][8], fa[kSwBwdRows], fbv[kSwBwdRows];
+#pragma unroll
+  for (int t = 0; t < 3; ++t)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cmax[t][j] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kSwBwdRows; ++i) {
+    float da[8], db[8], y[8];
+    grads(i, da, db, y);
+    float ma = 0.f, mb = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      ma = fmaxf(ma, fabsf(da[j]));
+      mb = fmaxf(mb, fabsf(db[j]));
+      if constexpr (COLS) {
+        cmax[0][j] = fmaxf(cmax[0][j], fabsf(da[j]));
+        cmax[1][j] = fmaxf(cmax[1][j], fabsf(db[j]));
+        cmax[2][j] = fmaxf(cmax[2][j], fabsf(y[j]));
+      }
+    }
+    ma = max16(ma);
+    mb = max16(mb);
+    const int row = r0 + STEP * i;
+    if (lane % 16 == 0 && row < p.M) {
+      p.sda[(size_t)tc * p.M + row] = fp8_scale<FMT>(ma);
+      p.sda[(size_t)(fb + tc) * p.M + row] = fp8_scale<FMT>(mb);
+    }
+    fa[i] = fp8_factor<FMT>(ma);
+    fbv[i] = fp8_factor<FMT>(mb);
+  }
+  if constexpr (COLS) {
+#pragma unroll
+    for (int t = 0; t < 3; ++t)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = fmaxf(cmax[t][j], __shfl_xor_sync(0xffffffffu, cmax[t][j], 16));
+        if (lane < 16) smax[warp][t][lane * 8 + j] = v;
+      }
+    __syncthreads();
+    if (threadIdx.x < 3 * 128) {
+      const int t = threadIdx.x / 128, c = threadIdx.x % 128;
+      float m = smax[0][t][c];
+#pragma unroll
+      for (int w = 1; w < kSwBwdThreads / 32; ++w) m = fmaxf(m, smax[w][t][c]);
+      if (t == 2) {
+        sfac[t][c] = fp8_factor<FP8_E4M3>(m);
+        p.syc[(size_t)tr * p.F + tc * 128 + c] = fp8_scale<FP8_E4M3>(m);
+      } else {
+        sfac[t][c] = fp8_factor<FMT>(m);
+        p.sdac[(size_t)tr * 2 * p.F + (size_t)t * p.F + tc * 128 + c] = fp8_scale<FMT>(m);
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < kSwBwdRows; ++i) {
+    const int row = r0 + STEP * i;
+    if (row >= p.M) continue;
+    float da[8], db[8], y[8];
+    grads(i, da, db, y);
+    const size_t oa = (size_t)row * 2 * p.F + c0, ob = oa + p.F;
+    stg_v2(p.da + oa, fp8_pack8<FMT>(da, fa[i]));
+    stg_v2(p.da + ob, fp8_pack8<FMT>(db, fbv[i]));
+    if constexpr (COLS) {
+      const int c = (lane % 16) * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        da[j] *= sfac[0][c + j];
+        db[j] *= sfac[1][c + j];
+        y[j] *= sfac[2][c + j];
+      }
+      stg_v2(p.dac + oa, fp8_pack8<FMT>(da, 1.f));
+      stg_v2(p.dac + ob, fp8_pack8<FMT>(db, 1.f));
+      stg_v2(p.yc + (size_t)row * p.F + c0, fp8_pack8<FP8_E4M3>(y, 1.f));
+    }
+  }
+}
+
+}  // namespace coda

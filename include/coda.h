@@ -126,6 +126,12 @@ coda_status coda_selftest_wait_timeout(void* ws, uint64_t limit_ns, void* stream
 #define CODA_KERNEL_ROWCOEF_REDUCE 20     /* c from its row partials (MLP block backward) */
 #define CODA_KERNEL_XENT_REDUCE 21        /* loss and log-sum-exp from the tile partials */
 #define CODA_KERNEL_ROPE_UNROTATE 22      /* inverse rotation of dQ, dK (RoPE backward) */
+#define CODA_KERNEL_GEMM_FP8 32           /* the 8-bit GEMM (coda_gemm_fp8) */
+#define CODA_KERNEL_GEMM_SWIGLU_FP8 33    /* the 8-bit gate/up GEMM with SwiGLU */
+#define CODA_KERNEL_QUANT_FP8 34          /* bf16 -> 8 bits (coda_quant_fp8, coda_quant_fp8_blocks) */
+#define CODA_KERNEL_SWIGLU_FP8_BWD 35     /* SwiGLU backward from the 8-bit [a | b] */
+#define CODA_KERNEL_RMSNORM_FP8_FWD 36    /* residual + RMSNorm -> 8 bits */
+#define CODA_KERNEL_RMSNORM_FP8_BWD 37    /* its backward (dg's column reduce is CODA_KERNEL_COL_REDUCE) */
 coda_status coda_profile_arm(int kernel, void* ev_start, void* ev_stop);
 
 /* ---------------------------------------------------------------- building block */
@@ -350,6 +356,96 @@ size_t coda_qkv_rope_bwd_workspace_bytes(int M, int d, int n_q, int n_kv, int he
 coda_status coda_qkv_rope_bwd(const void* dQKV, const void* X, const void* Wqkv, void* dX, void* dW, int M, int d,
                               int n_q, int n_kv, int head_dim, int seq_len, float base,
                               void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- 8-bit operands */
+
+/* The block's products on 8-bit floating-point operands with a scale for each
+ * block of 128 values, and the passes that make those operands.
+ *
+ * A block of values x is kept as q * S: with c = max(max |x|, 2^-100),
+ * S = c / fmax and q = x * (fmax / c) rounded to the nearest 8-bit number,
+ * fmax = 448 (CODA_FP8_E4M3) or 57344 (CODA_FP8_E5M2).  NaNs do not count
+ * towards max |x| and stay NaN; a block that holds an infinity comes back NaN.
+ * Three block forms of a stored matrix [R, C] (scales fp32, dense; the last
+ * block of a ragged axis is short):
+ *   rows     1 x 128     S [ceil(C/128), R]   operand whose columns are reduced over
+ *   columns  128 x 1     S [ceil(R/128), C]   operand whose rows are reduced over
+ *   blocks   128 x 128   S [ceil(R/128), ceil(C/128)]   weights, either way
+ * Row and column scales have the blocked axis first.  Nothing is transposed:
+ * a weight gradient dY^T X takes dY and X as they are stored, in columns form.
+ *
+ * Quantised matrices are dense, their column count a multiple of 16; any number
+ * of rows.  Outputs may not overlap inputs.  These calls allocate nothing and,
+ * but for the norm's backward, need no scratch; `ws` of the two products holds
+ * only the status word. */
+#define CODA_FP8_E4M3 0
+#define CODA_FP8_E5M2 1
+
+/* Rows and/or columns form of Z = diag(rowvec) X diag(colvec) in one pass over
+ * X [R, C] bf16 (rowvec fp32 [R], colvec bf16 [C], each optional: H, r and g
+ * give the columns form of the RMSNorm's output).  Qr, Sr: rows form; Qc, Sc:
+ * columns form; a pair may be NULL, not both pairs.  C % 16 == 0. */
+coda_status coda_quant_fp8(const void* X, const float* rowvec_or_null, const void* colvec_or_null,
+                           void* Qr_or_null, float* Sr_or_null, void* Qc_or_null, float* Sc_or_null,
+                           int R, int C, int format, void* stream);
+
+/* Blocks form of a weight W [R, C] bf16: Q [R, C], S [ceil(R/128), ceil(C/128)].  C % 16 == 0. */
+coda_status coda_quant_fp8_blocks(const void* W, void* Q, float* S, int R, int C, int format, void* stream);
+
+/* C[M,N] = op(A) op(B)^T over 8-bit operands, as coda_gemm:
+ *   a_mn_major = 0: A stored [M, K] in rows form;  1: A stored [K, M] in columns form.
+ *   b_mn_major = 0: B stored [N, K];               1: B stored [K, N].
+ *   b_blocks = 1: SB is the blocks form of B as it is stored; 0: the form that
+ *   blocks the reduction, SB [ceil(K/128), N].  SA is always [ceil(K/128), M].
+ * a_format, b_format: CODA_FP8_*, independent of each other.  Sums of 128 products are formed in
+ * the tensor cores, scaled and added in fp32.  c_fp32 = 0: C bf16.  c_fp32 = 1: C fp32, and with
+ * accumulate = 1 the product is added to C (gradient accumulation).
+ * Requires N % 16 == 0; K % 16 == 0 unless both operands are MN-major; M % 16 == 0 when a_mn_major.
+ * M = 0 or N = 0 does nothing; K = 0 writes zeros (adds nothing).  ws: coda_gemm_workspace_bytes(). */
+coda_status coda_gemm_fp8(const void* A, const float* SA, const void* B, const float* SB, void* C, int M, int N, int K,
+                          int a_mn_major, int b_mn_major, int a_format, int b_format, int b_blocks, int c_fp32,
+                          int accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* coda_gemm_swiglu on 8-bit operands: [a | b] = A Wgu^T, Y = silu(a) * b, all e4m3.
+ * A [M, K] in rows form, Wgu [2F, K] (gate rows first) in blocks form.  Outputs
+ * Y [M, F] in rows form, SY [F/128, M] (the down projection's operand), and the
+ * backward's checkpoint AB [M, 2F] in rows form, SAB [2F/128, M] (both NULL to
+ * skip), half the bytes of a bf16 [a | b].
+ * Requires K % 16 == 0, F % 128 == 0.  ws: coda_gemm_workspace_bytes(). */
+coda_status coda_gemm_swiglu_fp8(const void* A, const float* SA, const void* Wgu, const float* SW,
+                                 void* Y, float* SY, void* AB_or_null, float* SAB_or_null,
+                                 int M, int K, int F, void* ws, size_t ws_bytes, void* stream);
+
+/* SwiGLU backward from the 8-bit checkpoint: with a, b the saved values,
+ * s = sigmoid(a): da = dY b s (1 + a (1 - s)), db = dY a s.  dY [M, F] bf16.
+ * Outputs dA = [da | db] [M, 2F] in rows form with SdA [2F/128, M] (operand of
+ * the input gradient), and, all four or none, dAc [M, 2F] with SdAc
+ * [ceil(M/128), 2F] and Yc [M, F] with SYc [ceil(M/128), F] in columns form
+ * (operands of the two weight gradients; Yc = silu(a) b of the saved values,
+ * e4m3).  `format` is dA's and dAc's.  Requires F % 128 == 0. */
+coda_status coda_swiglu_fp8_bwd(const void* dY, const void* AB, const float* SAB, void* dA, float* SdA,
+                                void* dAc_or_null, float* SdAc_or_null, void* Yc_or_null, float* SYc_or_null,
+                                int M, int F, int format, void* stream);
+
+/* RMSNorm with the residual's addition and an 8-bit output: H = bf16(X + R)
+ * (R and H both NULL: H is X and is not written), r_i = 1/sqrt(mean_j H_ij^2 +
+ * eps) from the stored H, n = H_ij r_i g_j as Q [M, d] e4m3 in rows form with
+ * S [ceil(d/128), M].  X, R, H [M, d] and g [d] bf16; r [M] fp32.
+ * Requires d % 16 == 0, d <= 32768, eps > 0. */
+coda_status coda_rmsnorm_fp8_fwd(const void* X, const void* R_or_null, const void* g, void* H_or_null, float* r,
+                                 void* Q, float* S, int M, int d, float eps, void* stream);
+
+/* Workspace for coda_rmsnorm_fp8_bwd: status word and the partial sums of dg. */
+size_t coda_rmsnorm_fp8_bwd_workspace_bytes(int M, int d);
+
+/* Its backward; the rounding to 8 bits passes gradients straight through.
+ * dN [M, d] bf16 is the gradient of n:  u = dN g;
+ * dH = r u - H r^3 mean_j(u H) (+ dH_in, the gradient that arrives at H);
+ * dg_j = sum_i dN_ij H_ij r_i (fp32 [d], summed in a fixed order).  dH (bf16) is
+ * the gradient of both X and R. */
+coda_status coda_rmsnorm_fp8_bwd(const void* dN, const void* H, const float* r, const void* g,
+                                 const void* dH_in_or_null, void* dH, float* dg, int M, int d,
+                                 void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- unfused comparison sequence */
 
