@@ -19,9 +19,11 @@
 // and in the gate/up product 64 gate columns beside the same 64 up columns.
 //
 // Roles (384 threads, one CTA per SM): warp 0 TMA producer; warp 1 TMEM owner
-// and MMA issuer (pair's leader); warps 4-7 drain half 0, warps 8-11 half 1,
+// and MMA issuer (pair's leader); warp 2 copies the scales of the blocks ahead
+// into a ring of their own (read by the drain directly, their latency was paid
+// once per 128 of k: 743 us against NEWTIME for the 7B down projection); warps 4-7 drain half 0, warps 8-11 half 1,
 // one output row and 128 columns (128 fp32 registers) per thread.  The first
-// warpgroup hands registers to the other two: 128 x 72 + 256 x 216 is the
+// warpgroup hands registers to the other two: 128 x 40 + 256 x 232 is the
 // launch's 384 x 168.  Waits are bounded (mbar_wait); a role that gives up
 // records it and the CTA drains and exits.
 #pragma once
@@ -34,7 +36,7 @@ namespace coda {
 constexpr int F8_BK = 128;          // reduction depth of a stage and of a scale block
 constexpr int F8_UMMA_K = 32;
 constexpr int F8_THREADS = 384;
-constexpr int F8_REGS_ISSUE = 72, F8_REGS_DRAIN = 216;
+constexpr int F8_REGS_ISSUE = 40, F8_REGS_DRAIN = 232;
 static_assert(128 * F8_REGS_ISSUE + 256 * F8_REGS_DRAIN <= 384 * 168, "registers of the launch");
 constexpr int F8_STAGES = 5;
 constexpr int F8_A_BYTES = 128 * F8_BK;
@@ -44,10 +46,12 @@ constexpr int F8_EPI_WARPS = 8;
 constexpr int F8_SLOTS = 3;                    // staging tiles per epilogue warp
 constexpr int F8_SLOT_BYTES = 32 * 64;         // 32 rows x 64 bytes
 constexpr int F8_WARP_STAGING = F8_SLOTS * F8_SLOT_BYTES;
-constexpr int F8_VEC_BYTES = F8_EPI_WARPS * 2 * 128 * 4;  // column scales: 2 x 128 floats per warp
+constexpr int F8_SCALE_STAGES = 6;
+constexpr int F8_SCALE_FLOATS = 128 + 256;     // row scales, column scales (or two block scales)
+constexpr int F8_SCALE_BYTES = F8_SCALE_STAGES * F8_SCALE_FLOATS * 4;
 constexpr int F8_XCH_BYTES = 2 * 2 * 3 * 128 * 4;         // row maxima of the two halves, double-buffered
 constexpr int F8_SMEM_BYTES =
-    F8_STAGES * F8_STAGE_BYTES + F8_EPI_WARPS * F8_WARP_STAGING + F8_VEC_BYTES + F8_XCH_BYTES + 1024 + 256;
+    F8_STAGES * F8_STAGE_BYTES + F8_EPI_WARPS * F8_WARP_STAGING + F8_SCALE_BYTES + F8_XCH_BYTES + 1024 + 256;
 static_assert(F8_SMEM_BYTES <= 232448, "shared memory of one CTA");
 
 enum F8Epi : int {
@@ -96,21 +100,48 @@ __device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 
-// 16 accumulator columns of this thread's TMEM lane; valid after tmem_wait_ld.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+// 64 accumulator columns of this thread's TMEM lane; valid after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(taddr)
       : "memory");
 }
 // Wait for every TMEM load of this thread; ties `r` to a point after the wait.
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[64]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i])::"memory");
+  for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(r[i])::"memory");
+}
+
+// Asynchronous 4- or 16-byte copy to shared memory; zeros when !valid.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void* dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES),
+               "r"(valid ? BYTES : 0)
+               : "memory");
+}
+// Arrive on `bar` (whose count includes this thread) when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Hand a drained TMEM buffer to the pair's leader.  What is handed over are TMEM
+// loads that tcgen05.wait::ld has completed, no ordinary memory, so the arrival
+// needs no cluster-scope release: that one waits for a memory barrier, once per
+// 128 of k.
+__device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0)) : "memory");
 }
 
 // Packed pairs of floats: one instruction for two multiply-adds.
@@ -142,27 +173,30 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
 
 // acc[0..63] (128 columns in pairs) += TMEM columns times lo (columns 0-63) or
 // hi (64-127); with VEC the columns have scales of their own in cs[128]
-// (shared memory).  16 columns are in flight while the 16 before them are added.
-template <bool VEC>
-__device__ __forceinline__ void f8_promote(uint32_t taddr, float lo, float hi, const float* cs, uint64_t (&acc)[64]) {
-  const uint64_t s2[2] = {pack_f32x2(lo, lo), pack_f32x2(hi, hi)};
-  uint32_t v[2][16];
-  tmem_ld16(taddr, v[0]);
+// (shared memory).  Two loads of 64 columns: each exposes its latency once, and
+// the buffer is handed back (release) as soon as the second has arrived.
+template <bool VEC, typename Release>
+__device__ __forceinline__ void f8_promote(uint32_t taddr, float lo, float hi, const float* cs, uint64_t (&acc)[64],
+                                           Release release) {
+  uint32_t v[64];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    tmem_wait_ld(v[c & 1]);
-    if (c < 7) tmem_ld16(taddr + (c + 1) * 16, v[(c + 1) & 1]);
+  for (int c = 0; c < 2; ++c) {
+    tmem_ld64(taddr + c * 64, v);
+    tmem_wait_ld(v);
+    if (c == 1) release();
+    const float s = c ? hi : lo;
+    const uint64_t s2 = pack_f32x2(s, s);
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      uint64_t x = pack_u32x2(v[c & 1][2 * i], v[c & 1][2 * i + 1]);
-      uint64_t y = pack_u32x2(v[c & 1][2 * i + 2], v[c & 1][2 * i + 3]);
+    for (int i = 0; i < 32; i += 2) {
+      uint64_t x = pack_u32x2(v[2 * i], v[2 * i + 1]);
+      uint64_t y = pack_u32x2(v[2 * i + 2], v[2 * i + 3]);
       if constexpr (VEC) {
-        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(cs + c * 16 + 2 * i);
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(cs + c * 64 + 2 * i);
         x = mul_f32x2(x, q.x);
         y = mul_f32x2(y, q.y);
       }
-      acc[c * 8 + i] = fma_f32x2(x, s2[c / 4], acc[c * 8 + i]);
-      acc[c * 8 + i + 1] = fma_f32x2(y, s2[c / 4], acc[c * 8 + i + 1]);
+      acc[c * 32 + i] = fma_f32x2(x, s2, acc[c * 32 + i]);
+      acc[c * 32 + i + 1] = fma_f32x2(y, s2, acc[c * 32 + i + 1]);
     }
   }
 }
@@ -221,14 +255,16 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   uint8_t* sA = smem;
   uint8_t* sB = sA + S * F8_A_BYTES;
   uint8_t* sEpi = sB + S * F8_B_BYTES;
-  float* sVec = reinterpret_cast<float*>(sEpi + F8_EPI_WARPS * F8_WARP_STAGING);
-  float* sXch = sVec + F8_VEC_BYTES / 4;
+  float* sScale = reinterpret_cast<float*>(sEpi + F8_EPI_WARPS * F8_WARP_STAGING);
+  float* sXch = sScale + F8_SCALE_BYTES / 4;
   uint64_t* full = reinterpret_cast<uint64_t*>(sXch + F8_XCH_BYTES / 4);
   uint64_t* empty = full + S;
   uint64_t* tfull = empty + S;   // [2 * parity + half]
   uint64_t* tempty = tfull + 4;
   uint64_t* xch = tempty + 4;
-  uint64_t* mma_done = xch + 1;
+  uint64_t* sfull = xch + 1;
+  uint64_t* sempty = sfull + F8_SCALE_STAGES;
+  uint64_t* mma_done = sempty + F8_SCALE_STAGES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -248,6 +284,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       mbar_init(&tempty[a], 8);  // four warps of each CTA
     }
     mbar_init(xch, F8_EPI_WARPS);
+    for (int a = 0; a < F8_SCALE_STAGES; ++a) {
+      mbar_init(&sfull[a], 32);
+      mbar_init(&sempty[a], F8_EPI_WARPS);
+    }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -351,20 +391,66 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       }
       umma_commit_pair(mapa_shared(smem_u32(mma_done), 0));
       mbar_wait(mma_done, 0, ctl, 1, kWaitDrain);
+    } else if (warp == 2) {
+      // ---------------------------------------------------------------- scales (both CTAs)
+      int st = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
+        int m_blk, n_blk;
+        tile_coords(tile, p.num_m_tiles, p.num_n_tiles, p.group_m, m_blk, n_blk);
+        const int row = m_blk * 256 + (int)rank * 128 + lane;
+        const float* sb = p.sb;
+        bool sbv = true;
+        if constexpr (VEC) {
+          sb += n_blk * 256 + lane * 4;
+        } else {
+          // Lane h: the block of half h, or (gate/up) of the gate columns and of the up columns.
+          const int nb = EPI == F8_EPI_SWIGLU ? n_blk + lane * (p.split / 128) : n_blk * 2 + lane;
+          sbv = lane < 2 && (EPI == F8_EPI_SWIGLU || nb * 128 < p.N);
+          sb += sbv ? (size_t)nb * p.sb_n : 0;
+        }
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          ok = mbar_wait(&sempty[st], phase ^ 1u, ctl, 6, kWaitEmpty);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          float* dst = sScale + st * F8_SCALE_FLOATS;
+          const float* sa = p.sa + (size_t)kb * p.M;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool v = row + 32 * i < p.M;
+            cp_async<4>(dst + 32 * i + lane, sa + (v ? row + 32 * i : 0), v);
+          }
+          if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const bool v = n_blk * 256 + 128 * i + lane * 4 < p.N;
+              cp_async<16>(dst + 128 + 128 * i + lane * 4, v ? sb + (size_t)kb * p.N + 128 * i : p.sb, v);
+            }
+          } else {
+            if (lane < 2) cp_async<4>(dst + 128 + lane, sb + (sbv ? (size_t)kb * p.sb_k : 0), sbv);
+          }
+          cp_async_arrive(&sfull[st]);
+          if (++st == F8_SCALE_STAGES) {
+            st = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
     // ---------------------------------------------------------------- drain and epilogue (both CTAs)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F8_REGS_DRAIN));
     const int q = warp & 3;           // TMEM lane quarter this warp may access
     const int h = (warp - 4) / 4;     // column half
-    float* vec = sVec + (warp - 4) * 256;
     F8Store es;
     es.stg = sEpi + (warp - 4) * F8_WARP_STAGING;
     es.lane = lane;
     es.rows = p.M;
     es.slot = 0;
-    uint32_t it = 0, tiles_done = 0;
-    int stage = 0;
+    uint32_t it = 0, tiles_done = 0, sphase = 0;
+    int stage = 0, sst = 0;
     bool ok = true;
     for (int tile = first_tile; tile < num_tiles; tile += tile_step, ++tiles_done) {
       int m_blk, n_blk;
@@ -373,35 +459,19 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       const int row = row0 + lane;
       const bool rv = row < p.M;
       const int col0 = EPI == F8_EPI_SWIGLU ? n_blk * 128 + h * 64 : n_blk * 256 + h * 128;
-      const float* sa = p.sa + (rv ? row : 0);
-      // Weight blocks: half h is one 128-column block; the gate/up halves hold
-      // 64 columns of a gate block and 64 of the up block F rows below it.
-      const float* sb = p.sb;
-      const float* sb2 = p.sb;
-      if constexpr (!VEC) {
-        const int nb = EPI == F8_EPI_SWIGLU ? n_blk : min(n_blk * 2 + h, (p.N + 127) / 128 - 1);
-        sb += (size_t)nb * p.sb_n;
-        if constexpr (EPI == F8_EPI_SWIGLU) sb2 = p.sb + (size_t)(nb + p.split / 128) * p.sb_n;
-      }
       uint64_t acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0ull;
       for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
-        const float a_s = rv ? __ldg(sa + (size_t)kb * p.M) : 0.f;
-        float b_s = 1.f, b_s2 = 1.f;
-        float* cs = vec + (it & 1) * 128;
-        if constexpr (VEC) {
-          const int c = col0 + lane * 4;
-          float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (c < p.N) f = __ldg(reinterpret_cast<const float4*>(p.sb + (size_t)kb * p.N + c));
-          *reinterpret_cast<float4*>(cs + lane * 4) = f;
-          __syncwarp();
-        } else {
-          b_s = __ldg(sb + (size_t)kb * p.sb_k);
-          if constexpr (EPI == F8_EPI_SWIGLU) b_s2 = __ldg(sb2 + (size_t)kb * p.sb_k);
-        }
+        const float* sc = sScale + sst * F8_SCALE_FLOATS;
+        ok = mbar_wait(&sfull[sst], sphase, ctl, 2 + q, kWaitFull);
+        const float a_s = sc[q * 32 + lane];
+        const float* cs = sc + 128 + (VEC ? h * 128 : 0);
+        // Half h is one block of a weight; a gate/up half holds columns of a gate and of an up block.
+        const float b_lo = VEC ? 1.f : (EPI == F8_EPI_SWIGLU ? cs[0] : cs[h]);
+        const float b_hi = EPI == F8_EPI_SWIGLU ? cs[1] : b_lo;
         const int buf = (int)(it & 1) * 2 + h;
-        ok = mbar_wait(&tfull[buf], (it >> 1) & 1u, ctl, 2 + q, kWaitAccFull);
+        ok = ok && mbar_wait(&tfull[buf], (it >> 1) & 1u, ctl, 2 + q, kWaitAccFull);
         ok = __all_sync(0xffffffffu, ok);  // tcgen05.ld below needs all 32 lanes converged
         if (!ok) break;
         tc_fence_after();
@@ -409,11 +479,18 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         // tiles have been read and each CTA frees its own stage.
         if (warp == 8 && lane == 0) mbar_arrive(&empty[stage]);
         const uint32_t taddr = tmem_base + (uint32_t)(buf * 128) + ((uint32_t)(q * 32) << 16);
-        f8_promote<VEC>(taddr, a_s * b_s, a_s * (EPI == F8_EPI_SWIGLU ? b_s2 : b_s), cs, acc);
-        tc_fence_before();
+        f8_promote<VEC>(taddr, a_s * b_lo, a_s * b_hi, cs, acc, [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_leader(&tempty[buf]);
+        });
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[buf]), 0));
+        if (lane == 0) mbar_arrive(&sempty[sst]);
         if (++stage == S) stage = 0;
+        if (++sst == F8_SCALE_STAGES) {
+          sst = 0;
+          sphase ^= 1u;
+        }
       }
       if (!ok) break;
       es.row0 = row0;
