@@ -90,13 +90,30 @@ __device__ __forceinline__ uint64_t make_sdesc_sw64(uint32_t saddr, uint32_t lbo
   return (make_sdesc_sw128(saddr, lbo, sbo) & ~((uint64_t)7 << 61)) | ((uint64_t)4 << 61);
 }
 
-__device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// True in one lane of a converged warp.  The MMA issuer is chosen this way:
+// behind it the compiler knows that a single thread runs and keeps the
+// descriptors in uniform registers.  Behind `lane == 0` an MMA took 120 clocks
+// to issue whatever its size, which held the 8-bit product at half its rate.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
+// D = A B^T over one 128-deep stage: four MMAs of K = 32, A_STEP and B_STEP the
+// descriptors' advance between them (bytes / 16).
+template <int A_STEP, int B_STEP>
+__device__ __forceinline__ void umma_f8_stage_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .b64 a, b;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, 0;\n\t"
+      "add.u64 a, %1, %4;\n\tadd.u64 b, %2, %5;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, 1;\n\t"
+      "add.u64 a, %1, 2 * %4;\n\tadd.u64 b, %2, 2 * %5;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, 1;\n\t"
+      "add.u64 a, %1, 3 * %4;\n\tadd.u64 b, %2, 3 * %5;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, 1;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(A_STEP), "n"(B_STEP)
       : "memory");
 }
 
@@ -348,11 +365,13 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
           }
         }
       }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0 && elect_one()) {
       // ---------------------------------------------------------------- MMA issuer (pair's leader)
       int stage = 0;
       uint32_t phase = 0;
       uint32_t it = 0;  // 128-deep blocks issued: parity selects the TMEM buffers
+      const uint64_t a_desc0 = make_sdesc_sw128(smem_u32(sA), 16, 1024);
+      const uint64_t b_desc0 = B_MN ? make_sdesc_sw64(smem_u32(sB), 16, 512) : make_sdesc_sw128(smem_u32(sB), 16, 1024);
       bool ok = true;
       for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
         for (int kb = 0; kb < p.k_blocks && ok; ++kb, ++it) {
@@ -360,8 +379,6 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             ok = false;
             break;
           }
-          const uint32_t a_base = smem_u32(sA + stage * F8_A_BYTES);
-          const uint32_t b_base = smem_u32(sB + stage * F8_B_BYTES);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int buf = (int)(it & 1) * 2 + h;
@@ -370,17 +387,11 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
               break;
             }
             tc_fence_after();
-            const uint32_t d_tmem = tmem_base + (uint32_t)(buf * 128);
-#pragma unroll
-            for (int k = 0; k < F8_BK / F8_UMMA_K; ++k) {
-              // K-major: 32 bytes inside the 128-byte swizzled row; MN-major: 32
-              // k rows of 128 bytes (A) or 64 bytes (B, one 64-row half per CTA).
-              const uint64_t ad = A_MN ? make_sdesc_sw128(a_base + k * 4096, 16, 1024)
-                                       : make_sdesc_sw128(a_base + k * 32, 16, 1024);
-              const uint64_t bd = B_MN ? make_sdesc_sw64(b_base + h * 8192 + k * 2048, 16, 512)
-                                       : make_sdesc_sw128(b_base + h * 8192 + k * 32, 16, 1024);
-              umma_f8_pair(d_tmem, ad, bd, p.idesc, k > 0 ? 1u : 0u);
-            }
+            // K-major: 32 bytes inside the 128-byte swizzled row; MN-major: 32 k
+            // rows of 128 bytes (A) or 64 bytes (B, one 64-row half per CTA).
+            umma_f8_stage_pair<A_MN ? 256 : 2, B_MN ? 128 : 2>(
+                tmem_base + (uint32_t)(buf * 128), a_desc0 + (uint64_t)(stage * (F8_A_BYTES >> 4)),
+                b_desc0 + (uint64_t)(stage * (F8_B_BYTES >> 4) + h * (8192 >> 4)), p.idesc);
             umma_commit_pair_both(&tfull[buf]);
           }
           if (++stage == S) {
