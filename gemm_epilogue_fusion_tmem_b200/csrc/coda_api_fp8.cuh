@@ -11,26 +11,26 @@ namespace {
 
 constexpr int kScaleBlock = 128;  // values per scale along a blocked axis
 
-// Encoded maps of the 8-bit path, cached per host thread as make_tmap's are;
-// rows of `cols` elements, `ld` elements apart.
+// Encoded maps of the 8-bit operands, cached per host thread as make_tmap's are.
 struct Tmap8Slot {
   const void* base;
-  long long rows, cols, ld;
-  int dtype, box_cols, box_rows, swizzle;
+  long long rows, cols;
+  int box_cols, box_rows, swizzle;
   CUtensorMap map;
   bool valid;
 };
 constexpr int kTmap8Slots = 128;
 thread_local Tmap8Slot t_tmap8_cache[kTmap8Slots];
 
-bool make_tmap8(CUtensorMap* m, CUtensorMapDataType dtype, int elem_bytes, const void* base, long long rows,
-                long long cols, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
+// 8-bit matrix [rows][cols], boxes of box_cols x box_rows; out-of-range elements load as zero.
+bool make_tmap8(CUtensorMap* m, const void* base, long long rows, long long cols, int box_cols, int box_rows,
+                CUtensorMapSwizzle swizzle) {
   uint64_t h = reinterpret_cast<uintptr_t>(base) >> 4;
   for (uint64_t v : {(uint64_t)rows, (uint64_t)cols, (uint64_t)box_cols * 1024 + (uint64_t)box_rows,
-                     (uint64_t)swizzle * 64 + (uint64_t)dtype})
+                     (uint64_t)swizzle})
     h = (h ^ v) * 0x9E3779B97F4A7C15ull;
   Tmap8Slot& s = t_tmap8_cache[(h >> 32) % kTmap8Slots];
-  if (s.valid && s.base == base && s.rows == rows && s.cols == cols && s.dtype == (int)dtype &&
+  if (s.valid && s.base == base && s.rows == rows && s.cols == cols &&
       s.box_cols == box_cols && s.box_rows == box_rows && s.swizzle == (int)swizzle) {
     *m = s.map;
     return true;
@@ -38,16 +38,15 @@ bool make_tmap8(CUtensorMap* m, CUtensorMapDataType dtype, int elem_bytes, const
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)cols * elem_bytes};
+  cuuint64_t strides[1] = {(cuuint64_t)cols};
   cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
-  if (enc(m, dtype, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+  if (enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return false;
   s.base = base;
   s.rows = rows;
   s.cols = cols;
-  s.dtype = (int)dtype;
   s.box_cols = box_cols;
   s.box_rows = box_rows;
   s.swizzle = (int)swizzle;
@@ -56,17 +55,15 @@ bool make_tmap8(CUtensorMap* m, CUtensorMapDataType dtype, int elem_bytes, const
   return true;
 }
 
-constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-
 // A operand [m, k]: one box of 128 k x 128 m.  B operand [n, k]: boxes of 64 n
 // (a CTA's share of one column half).
 bool operand8_map_a(CUtensorMap* m, const void* p, long long mn, long long k, bool mn_major) {
-  if (mn_major) return make_tmap8(m, kU8, 1, p, k, mn, 128, F8_BK, CU_TENSOR_MAP_SWIZZLE_128B);
-  return make_tmap8(m, kU8, 1, p, mn, k, F8_BK, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (mn_major) return make_tmap8(m, p, k, mn, 128, F8_BK, CU_TENSOR_MAP_SWIZZLE_128B);
+  return make_tmap8(m, p, mn, k, F8_BK, 128, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 bool operand8_map_b(CUtensorMap* m, const void* p, long long mn, long long k, bool mn_major) {
-  if (mn_major) return make_tmap8(m, kU8, 1, p, k, mn, 64, F8_BK, CU_TENSOR_MAP_SWIZZLE_64B);
-  return make_tmap8(m, kU8, 1, p, mn, k, F8_BK, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (mn_major) return make_tmap8(m, p, k, mn, 64, F8_BK, CU_TENSOR_MAP_SWIZZLE_64B);
+  return make_tmap8(m, p, mn, k, F8_BK, 64, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Rasterisation as pick_group, in bytes of 8-bit operands.
@@ -80,8 +77,7 @@ int pick_group8(long long a_rows, long long b_rows, int num_m, int num_n, int k_
 }
 
 template <int EPI, bool A_MN, bool B_MN, bool VEC>
-coda_status launch_gemm8(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to1, const CUtensorMap& to2,
-                         Gemm8Params p, cudaStream_t s) {
+coda_status launch_gemm8(const CUtensorMap& ta, const CUtensorMap& tb, Gemm8Params p, cudaStream_t s) {
   static std::atomic<int> clusters_of[kMaxDevices];  // 0: not set up on this device yet
   int dev = 0;
   coda_status st = current_device(dev);
@@ -114,20 +110,21 @@ coda_status launch_gemm8(const CUtensorMap& ta, const CUtensorMap& tb, const CUt
   const int units = (int)std::min<long long>(tiles, clusters);
   g_launch_tag = EPI == F8_EPI_SWIGLU ? CODA_KERNEL_GEMM_SWIGLU_FP8 : CODA_KERNEL_GEMM_FP8;
   const cudaError_t e =
-      launch_ex(kern, dim3(2 * units), dim3(F8_THREADS), F8_SMEM_BYTES, s, 2, ta, tb, to1, to2, p);
+      launch_ex(kern, dim3(2 * units), dim3(F8_THREADS), F8_SMEM_BYTES, s, 2, ta, tb, p);
   g_launch_tag = -1;
   return e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess ? CODA_OK : CODA_ERR_CUDA;
 }
 
 template <int EPI, bool VEC>
-coda_status launch_gemm8_majors(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to, bool a_mn,
-                                bool b_mn, const Gemm8Params& p, cudaStream_t s) {
-  if (!a_mn && !b_mn) return launch_gemm8<EPI, false, false, VEC>(ta, tb, to, to, p, s);
-  if (!a_mn && b_mn) return launch_gemm8<EPI, false, true, VEC>(ta, tb, to, to, p, s);
-  if (a_mn && b_mn) return launch_gemm8<EPI, true, true, VEC>(ta, tb, to, to, p, s);
-  return launch_gemm8<EPI, true, false, VEC>(ta, tb, to, to, p, s);
+coda_status launch_gemm8_majors(const CUtensorMap& ta, const CUtensorMap& tb, bool a_mn, bool b_mn,
+                                const Gemm8Params& p, cudaStream_t s) {
+  if (!a_mn && !b_mn) return launch_gemm8<EPI, false, false, VEC>(ta, tb, p, s);
+  if (!a_mn && b_mn) return launch_gemm8<EPI, false, true, VEC>(ta, tb, p, s);
+  if (a_mn && b_mn) return launch_gemm8<EPI, true, true, VEC>(ta, tb, p, s);
+  return launch_gemm8<EPI, true, false, VEC>(ta, tb, p, s);
 }
 
+inline bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 inline bool known_format(int f) { return f == CODA_FP8_E4M3 || f == CODA_FP8_E5M2; }
 inline bool tiles_fit(long long a, long long b) { return a * b <= 0x7FFFFFFFLL; }
 
@@ -257,11 +254,8 @@ coda_status coda_gemm_fp8(const void* A, const float* SA, const void* B, const f
   int dev;
   CODA_TRY(current_device(dev));
   const bool a_mn = a_mn_major != 0, b_mn = b_mn_major != 0;
-  CUtensorMap ta, tb, to;
+  CUtensorMap ta, tb;
   if (!operand8_map_a(&ta, A, M, K, a_mn) || !operand8_map_b(&tb, B, N, K, b_mn)) return CODA_ERR_CUDA;
-  if (!(c_fp32 ? make_tmap8(&to, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, C, M, N, 16, 32, CU_TENSOR_MAP_SWIZZLE_64B)
-               : make_tmap8(&to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, C, M, N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)))
-    return CODA_ERR_CUDA;
   Gemm8Params p;
   std::memset(&p, 0, sizeof(p));
   p.M = M;
@@ -277,14 +271,16 @@ coda_status coda_gemm_fp8(const void* A, const float* SA, const void* B, const f
   p.sb_n = b_mn ? 1 : p.k_blocks;
   p.sb_k = b_mn ? cdiv(N, kScaleBlock) : 1;
   p.add = accumulate;
+  p.out = C;
+  p.wide = aligned32(C);
   p.idesc = make_idesc_f8(256, 128, a_format, b_format, a_mn, b_mn);
   p.status = static_cast<uint32_t*>(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (c_fp32)
-    return b_blocks ? launch_gemm8_majors<F8_EPI_F32, false>(ta, tb, to, a_mn, b_mn, p, s)
-                    : launch_gemm8_majors<F8_EPI_F32, true>(ta, tb, to, a_mn, b_mn, p, s);
-  return b_blocks ? launch_gemm8_majors<F8_EPI_BF16, false>(ta, tb, to, a_mn, b_mn, p, s)
-                  : launch_gemm8_majors<F8_EPI_BF16, true>(ta, tb, to, a_mn, b_mn, p, s);
+    return b_blocks ? launch_gemm8_majors<F8_EPI_F32, false>(ta, tb, a_mn, b_mn, p, s)
+                    : launch_gemm8_majors<F8_EPI_F32, true>(ta, tb, a_mn, b_mn, p, s);
+  return b_blocks ? launch_gemm8_majors<F8_EPI_BF16, false>(ta, tb, a_mn, b_mn, p, s)
+                  : launch_gemm8_majors<F8_EPI_BF16, true>(ta, tb, a_mn, b_mn, p, s);
 }
 
 coda_status coda_gemm_swiglu_fp8(const void* A, const float* SA, const void* Wgu, const float* SW, void* Y, float* SY,
@@ -302,12 +298,8 @@ coda_status coda_gemm_swiglu_fp8(const void* A, const float* SA, const void* Wgu
   if (ws_bytes < coda_gemm_workspace_bytes()) return CODA_ERR_WORKSPACE_TOO_SMALL;
   int dev;
   CODA_TRY(current_device(dev));
-  CUtensorMap ta, tb, to1, to2;
+  CUtensorMap ta, tb;
   if (!operand8_map_a(&ta, A, M, K, false) || !operand8_map_b(&tb, Wgu, 2LL * F, K, false)) return CODA_ERR_CUDA;
-  if (!make_tmap8(&to1, kU8, 1, Y, M, F, 64, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return CODA_ERR_CUDA;
-  to2 = to1;
-  if (AB_or_null && !make_tmap8(&to2, kU8, 1, AB_or_null, M, 2LL * F, 64, 32, CU_TENSOR_MAP_SWIZZLE_64B))
-    return CODA_ERR_CUDA;
   Gemm8Params p;
   std::memset(&p, 0, sizeof(p));
   p.M = M;
@@ -322,12 +314,14 @@ coda_status coda_gemm_swiglu_fp8(const void* A, const float* SA, const void* Wgu
   p.sb_n = p.k_blocks;
   p.sb_k = 1;
   p.split = F;
-  p.save_ab = AB_or_null != nullptr;
+  p.out = Y;
+  p.out2 = AB_or_null;
+  p.wide = aligned32(Y) && aligned32(AB_or_null);
   p.sy = SY;
   p.sab = SAB_or_null;
   p.idesc = make_idesc_f8(256, 128, FP8_E4M3, FP8_E4M3, false, false);
   p.status = static_cast<uint32_t*>(ws);
-  return launch_gemm8<F8_EPI_SWIGLU, false, false, false>(ta, tb, to1, to2, p, static_cast<cudaStream_t>(stream));
+  return launch_gemm8<F8_EPI_SWIGLU, false, false, false>(ta, tb, p, static_cast<cudaStream_t>(stream));
 }
 
 // ------------------------------------------------------------------ SwiGLU backward

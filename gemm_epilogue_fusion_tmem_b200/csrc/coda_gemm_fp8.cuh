@@ -38,20 +38,18 @@ constexpr int F8_UMMA_K = 32;
 constexpr int F8_THREADS = 384;
 constexpr int F8_REGS_ISSUE = 40, F8_REGS_DRAIN = 232;
 static_assert(128 * F8_REGS_ISSUE + 256 * F8_REGS_DRAIN <= 384 * 168, "registers of the launch");
-constexpr int F8_STAGES = 5;
+constexpr int F8_STAGES = 6;
 constexpr int F8_A_BYTES = 128 * F8_BK;
 constexpr int F8_B_BYTES = 128 * F8_BK;
 constexpr int F8_STAGE_BYTES = F8_A_BYTES + F8_B_BYTES;
 constexpr int F8_EPI_WARPS = 8;
-constexpr int F8_SLOTS = 3;                    // staging tiles per epilogue warp
-constexpr int F8_SLOT_BYTES = 32 * 64;         // 32 rows x 64 bytes
-constexpr int F8_WARP_STAGING = F8_SLOTS * F8_SLOT_BYTES;
-constexpr int F8_SCALE_STAGES = 6;
-constexpr int F8_SCALE_FLOATS = 128 + 256;     // row scales, column scales (or two block scales)
-constexpr int F8_SCALE_BYTES = F8_SCALE_STAGES * F8_SCALE_FLOATS * 4;
-constexpr int F8_XCH_BYTES = 2 * 2 * 3 * 128 * 4;         // row maxima of the two halves, double-buffered
-constexpr int F8_SMEM_BYTES =
-    F8_STAGES * F8_STAGE_BYTES + F8_EPI_WARPS * F8_WARP_STAGING + F8_SCALE_BYTES + F8_XCH_BYTES + 1024 + 256;
+constexpr int F8_GROUP = 8;                     // 128-deep blocks whose scales are staged together
+constexpr int F8_SCALE_BYTES = 2 * F8_GROUP * (128 + 256) * 4;  // two groups of row and column scales
+constexpr int F8_SMEM_BYTES = F8_STAGES * F8_STAGE_BYTES + F8_SCALE_BYTES + 1024 + 256;
+// The gate/up product has no column scales; its halves exchange row maxima (two
+// buffers) in their place.
+constexpr int F8_XCH_FLOATS = 2 * 2 * 3 * 128;
+static_assert(2 * F8_GROUP * (128 + 2) + F8_XCH_FLOATS <= F8_SCALE_BYTES / 4, "scales and maxima share the room");
 static_assert(F8_SMEM_BYTES <= 232448, "shared memory of one CTA");
 
 enum F8Epi : int {
@@ -69,9 +67,11 @@ struct Gemm8Params {
   int sb_n, sb_k;
   int split;        // F8_EPI_SWIGLU: row offset of the up half in B (= F)
   int add;          // F8_EPI_F32: add to C
-  int save_ab;      // F8_EPI_SWIGLU
   float* sy;        // [F / 128, M]
   float* sab;       // [2 F / 128, M]
+  void* out;        // C, or Y
+  void* out2;       // AB, or null
+  int wide;         // out (and out2) 32-byte aligned
   uint32_t idesc;
   uint32_t* status;
   unsigned long long wait_limit_ns;
@@ -117,28 +117,23 @@ __device__ __forceinline__ void umma_f8_stage_pair(uint32_t d_tmem, uint64_t a_d
       : "memory");
 }
 
-// 64 accumulator columns of this thread's TMEM lane; valid after tmem_wait_ld.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
+// 32 accumulator columns of this thread's TMEM lane; valid after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float (&v)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(taddr)
       : "memory");
 }
-// Wait for every TMEM load of this thread; ties `r` to a point after the wait.
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[64]) {
+// Wait for every TMEM load of this thread; ties `v` to a point after the wait.
+__device__ __forceinline__ void tmem_wait_ld(float (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(r[i])::"memory");
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[i])::"memory");
 }
 
 // Asynchronous 4- or 16-byte copy to shared memory; zeros when !valid.
@@ -153,139 +148,131 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// mbar_wait for a converged warp on a barrier that is about to complete: polled
+// in a tight loop (a poll sleeps in hardware until the phase ends or some
+// microseconds have passed), the bounded wait behind it.  Uniform result.
+template <typename Params>
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, const Params& prm,
+                                               volatile int* abort_flag, uint32_t role, uint32_t reason) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+      "POLL:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+      "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 16;\n\t@q bra POLL;\n"
+      "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  if (__all_sync(0xffffffffu, ok != 0)) return true;
+  const WaitCtl c{abort_flag, prm.status, prm.wait_limit_ns, prm.kernel_id};
+  return __all_sync(0xffffffffu,
+                    mbar_wait(static_cast<uint64_t*>(__cvta_shared_to_generic(bar)), parity, c, role, reason));
+}
+// Arrive where `pred` is set, without a branch.
+__device__ __forceinline__ void mbar_arrive_if(uint32_t bar, uint32_t pred) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(
+                   bar),
+               "r"(pred)
+               : "memory");
+}
+
 // Hand a drained TMEM buffer to the pair's leader.  What is handed over are TMEM
 // loads that tcgen05.wait::ld has completed, no ordinary memory, so the arrival
 // needs no cluster-scope release: that one waits for a memory barrier, once per
 // 128 of k.
-__device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0)) : "memory");
+__device__ __forceinline__ void mbar_arrive_leader_if(uint32_t leader_bar, uint32_t pred) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(
+          leader_bar),
+      "r"(pred)
+      : "memory");
 }
 
-// Packed pairs of floats: one instruction for two multiply-adds.
-__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ uint64_t pack_u32x2(uint32_t lo, uint32_t hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-  return d;
-}
-__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
-// acc[0..63] (128 columns in pairs) += TMEM columns times lo (columns 0-63) or
-// hi (64-127); with VEC the columns have scales of their own in cs[128]
-// (shared memory).  Two loads of 64 columns: each exposes its latency once, and
-// the buffer is handed back (release) as soon as the second has arrived.
+// acc += TMEM columns times lo (columns 0-63) or hi (64-127); with VEC the
+// columns have scales of their own in cs[128] (shared memory).  32 columns are
+// in flight while the 32 before them are added; the buffer is handed back
+// (release) as soon as the last have arrived.  Plain multiply-adds: the packed
+// fma.f32x2 runs at the same rate, and the moves that pair its operands cost
+// more than the issue slots it saves (356 against 408 us, 7B down projection).
 template <bool VEC, typename Release>
-__device__ __forceinline__ void f8_promote(uint32_t taddr, float lo, float hi, const float* cs, uint64_t (&acc)[64],
+__device__ __forceinline__ void f8_promote(uint32_t taddr, float lo, float hi, const float* cs, float (&acc)[128],
                                            Release release) {
-  uint32_t v[64];
+  float v[2][32];
+  tmem_ld32_async(taddr, v[0]);
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    tmem_ld64(taddr + c * 64, v);
-    tmem_wait_ld(v);
-    if (c == 1) release();
-    const float s = c ? hi : lo;
-    const uint64_t s2 = pack_f32x2(s, s);
+  for (int c = 0; c < 4; ++c) {
+    tmem_wait_ld(v[c & 1]);
+    if (c < 3) tmem_ld32_async(taddr + (c + 1) * 32, v[(c + 1) & 1]);
+    else release();
+    const float s = c < 2 ? lo : hi;
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      uint64_t x = pack_u32x2(v[2 * i], v[2 * i + 1]);
-      uint64_t y = pack_u32x2(v[2 * i + 2], v[2 * i + 3]);
+    for (int i = 0; i < 32; i += 4) {
+      float* x = v[c & 1] + i;
       if constexpr (VEC) {
-        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(cs + c * 64 + 2 * i);
-        x = mul_f32x2(x, q.x);
-        y = mul_f32x2(y, q.y);
+        const float4 f = *reinterpret_cast<const float4*>(cs + c * 32 + i);
+        x[0] *= f.x;
+        x[1] *= f.y;
+        x[2] *= f.z;
+        x[3] *= f.w;
       }
-      acc[c * 32 + i] = fma_f32x2(x, s2, acc[c * 32 + i]);
-      acc[c * 32 + i + 1] = fma_f32x2(y, s2, acc[c * 32 + i + 1]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[c * 32 + i + j] = fmaf(x[j], s, acc[c * 32 + i + j]);
     }
   }
 }
 
-// Per-warp tile store: 32 rows x 64 bytes per slot (any element type), 16-byte
-// chunks swizzled as the tensor map's 64-byte swizzle, one TMA store (or
-// fp32 add) per slot.  Slots rotate, so a step waits only for the store issued
-// F8_SLOTS steps before it.
-struct F8Store {
-  uint8_t* stg;
-  int lane, row0, rows, slot;
-
-  __device__ __forceinline__ void put(const uint4 (&q)[4], const CUtensorMap* m, int x, bool add) {
-    static_assert(F8_SLOTS == 3, "the wait below leaves F8_SLOTS - 1 = 2 groups in flight");
-    if (lane == 0) bulk_wait_read_2();
-    __syncwarp();
-    uint8_t* t = stg + slot * F8_SLOT_BYTES;
-    const int sw = (lane >> 1) & 3;
+// 32 bytes of a row: whole sectors, so a row per thread needs no staging.
+__device__ __forceinline__ void f8_store32(void* dst, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    stg_v4(dst, make_uint4(w[0], w[1], w[2], w[3]));
+    stg_v4(static_cast<uint8_t*>(dst) + 16, make_uint4(w[4], w[5], w[6], w[7]));
+  }
+}
+__device__ __forceinline__ void f8_add16(float* dst, const float* f) {
+  asm volatile("red.global.add.v4.f32 [%0], {%1,%2,%3,%4};" ::"l"(dst), "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3])
+               : "memory");
+}
+// 64 floats of a row, times factor, as 64 8-bit values.
+template <typename Value>
+__device__ __forceinline__ void f8_store_row64(uint8_t* dst, bool wide, Value value) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t a = smem_u32(t + lane * 64 + ((j ^ sw) << 4));
-      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(q[j].x), "r"(q[j].y), "r"(q[j].z),
-                   "r"(q[j].w)
-                   : "memory");
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      if (row0 < rows) {
-        if (add)
-          asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                           reinterpret_cast<uint64_t>(m)),
-                       "r"(smem_u32(t)), "r"(x), "r"(row0)
-                       : "memory");
-        else
-          tma_store_2d_hint(m, t, x, row0, l2_policy_evict_first());
-      }
-      bulk_commit_group();  // an empty group keeps the count of groups in step with the slots
-    }
-    slot = slot + 1 == F8_SLOTS ? 0 : slot + 1;
+  for (int c = 0; c < 64; c += 32) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      w[i] = fp8_pack4<FP8_E4M3>(value(c + 4 * i), value(c + 4 * i + 1), value(c + 4 * i + 2), value(c + 4 * i + 3));
+    f8_store32(dst + c, w, wide);
   }
-  __device__ __forceinline__ void finish() {
-    if (lane == 0) bulk_wait_all();
-    __syncwarp();
-  }
-};
+}
 
 template <int EPI, bool A_MN, bool B_MN, bool VEC>
 __global__ void __launch_bounds__(F8_THREADS, 1)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const __grid_constant__ CUtensorMap tmO1, const __grid_constant__ CUtensorMap tmO2,
                     const Gemm8Params p) {
   constexpr int S = F8_STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = sA + S * F8_A_BYTES;
-  uint8_t* sEpi = sB + S * F8_B_BYTES;
-  float* sScale = reinterpret_cast<float*>(sEpi + F8_EPI_WARPS * F8_WARP_STAGING);
-  float* sXch = sScale + F8_SCALE_BYTES / 4;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sXch + F8_XCH_BYTES / 4);
+  float* sScale = reinterpret_cast<float*>(sB + S * F8_B_BYTES);
+  constexpr int GROUP_FLOATS = F8_GROUP * (128 + (VEC ? 256 : 2));
+  float* sXch = sScale + 2 * GROUP_FLOATS;
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sScale) + F8_SCALE_BYTES);
   uint64_t* empty = full + S;
   uint64_t* tfull = empty + S;   // [2 * parity + half]
   uint64_t* tempty = tfull + 4;
   uint64_t* xch = tempty + 4;
   uint64_t* sfull = xch + 1;
-  uint64_t* sempty = sfull + F8_SCALE_STAGES;
-  uint64_t* mma_done = sempty + F8_SCALE_STAGES;
+  uint64_t* sempty = sfull + 2;
+  uint64_t* mma_done = sempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x / 32;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0);  // known uniform
   const int lane = threadIdx.x % 32;
   const uint32_t rank = cluster_ctarank();  // 0 = the pair's leader
   const int first_tile = (int)cluster_id_x();
@@ -301,7 +288,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       mbar_init(&tempty[a], 8);  // four warps of each CTA
     }
     mbar_init(xch, F8_EPI_WARPS);
-    for (int a = 0; a < F8_SCALE_STAGES; ++a) {
+    for (int a = 0; a < 2; ++a) {
       mbar_init(&sfull[a], 32);
       mbar_init(&sempty[a], F8_EPI_WARPS);
     }
@@ -394,6 +381,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                 b_desc0 + (uint64_t)(stage * (F8_B_BYTES >> 4) + h * (8192 >> 4)), p.idesc);
             umma_commit_pair_both(&tfull[buf]);
           }
+          umma_commit_pair_both(&empty[stage]);  // both CTAs' operand tiles have been read
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
@@ -410,42 +398,40 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
         int m_blk, n_blk;
         tile_coords(tile, p.num_m_tiles, p.num_n_tiles, p.group_m, m_blk, n_blk);
-        const int row = m_blk * 256 + (int)rank * 128 + lane;
-        const float* sb = p.sb;
-        bool sbv = true;
-        if constexpr (VEC) {
-          sb += n_blk * 256 + lane * 4;
-        } else {
-          // Lane h: the block of half h, or (gate/up) of the gate columns and of the up columns.
-          const int nb = EPI == F8_EPI_SWIGLU ? n_blk + lane * (p.split / 128) : n_blk * 2 + lane;
-          sbv = lane < 2 && (EPI == F8_EPI_SWIGLU || nb * 128 < p.N);
-          sb += sbv ? (size_t)nb * p.sb_n : 0;
-        }
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
-          ok = mbar_wait(&sempty[st], phase ^ 1u, ctl, 6, kWaitEmpty);
-          ok = __all_sync(0xffffffffu, ok);
+        const int row0 = m_blk * 256 + (int)rank * 128;
+        const int col0 = n_blk * 256;
+        // Lane h: the block of half h, or (gate/up) of the gate columns and of the up columns.
+        const int nb = EPI == F8_EPI_SWIGLU ? n_blk + lane * (p.split / 128) : n_blk * 2 + lane;
+        const bool sbv = EPI == F8_EPI_SWIGLU || nb * 128 < p.N;
+        for (int kb0 = 0; kb0 < p.k_blocks; kb0 += F8_GROUP) {
+          ok = mbar_wait_warp(smem_u32(&sempty[st]), phase ^ 1u, p, abort_flag, 6, kWaitEmpty);
           if (!ok) break;
-          float* dst = sScale + st * F8_SCALE_FLOATS;
-          const float* sa = p.sa + (size_t)kb * p.M;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool v = row + 32 * i < p.M;
-            cp_async<4>(dst + 32 * i + lane, sa + (v ? row + 32 * i : 0), v);
-          }
-          if constexpr (VEC) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const bool v = n_blk * 256 + 128 * i + lane * 4 < p.N;
-              cp_async<16>(dst + 128 + 128 * i + lane * 4, v ? sb + (size_t)kb * p.N + 128 * i : p.sb, v);
+          float* dst = sScale + st * GROUP_FLOATS;
+          float* dst_b = dst + F8_GROUP * 128;
+          const int n = min(F8_GROUP, p.k_blocks - kb0);
+          // Rolled loops: this warpgroup has few registers.
+#pragma unroll 1
+          for (int j = 0; j < n; ++j) {
+            const float* sa = p.sa + (size_t)(kb0 + j) * p.M;
+#pragma unroll 1
+            for (int i = lane; i < 128; i += 32) {
+              const bool v = row0 + i < p.M;
+              cp_async<4>(dst + j * 128 + i, sa + (v ? row0 + i : 0), v);
             }
-          } else {
-            if (lane < 2) cp_async<4>(dst + 128 + lane, sb + (sbv ? (size_t)kb * p.sb_k : 0), sbv);
+            if constexpr (VEC) {
+              const float* sb = p.sb + (size_t)(kb0 + j) * p.N;
+#pragma unroll 1
+              for (int i = lane * 4; i < 256; i += 128) {
+                const bool v = col0 + i < p.N;
+                cp_async<16>(dst_b + j * 256 + i, sb + (v ? col0 + i : 0), v);
+              }
+            } else if (lane < 2) {
+              cp_async<4>(dst_b + j * 2 + lane, p.sb + (sbv ? (size_t)nb * p.sb_n + (size_t)(kb0 + j) * p.sb_k : 0), sbv);
+            }
           }
           cp_async_arrive(&sfull[st]);
-          if (++st == F8_SCALE_STAGES) {
-            st = 0;
-            phase ^= 1u;
-          }
+          st ^= 1;
+          phase ^= st == 0;
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -455,13 +441,11 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F8_REGS_DRAIN));
     const int q = warp & 3;           // TMEM lane quarter this warp may access
     const int h = (warp - 4) / 4;     // column half
-    F8Store es;
-    es.stg = sEpi + (warp - 4) * F8_WARP_STAGING;
-    es.lane = lane;
-    es.rows = p.M;
-    es.slot = 0;
-    uint32_t it = 0, tiles_done = 0, sphase = 0;
-    int stage = 0, sst = 0;
+    const uint32_t one = lane == 0;  // this warp's arrivals
+    const uint32_t tfull_h = smem_u32(&tfull[h]);
+    const uint32_t tempty_h = mapa_shared(smem_u32(&tempty[h]), 0);
+    const uint32_t taddr_h = tmem_base + (uint32_t)(h * 128) + ((uint32_t)(q * 32) << 16);
+    uint32_t it = 0, groups = 0, tiles_done = 0;
     bool ok = true;
     for (int tile = first_tile; tile < num_tiles; tile += tile_step, ++tiles_done) {
       int m_blk, n_blk;
@@ -470,81 +454,75 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       const int row = row0 + lane;
       const bool rv = row < p.M;
       const int col0 = EPI == F8_EPI_SWIGLU ? n_blk * 128 + h * 64 : n_blk * 256 + h * 128;
-      uint64_t acc[64];
+      float acc[128];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-      for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
-        const float* sc = sScale + sst * F8_SCALE_FLOATS;
-        ok = mbar_wait(&sfull[sst], sphase, ctl, 2 + q, kWaitFull);
-        const float a_s = sc[q * 32 + lane];
-        const float* cs = sc + 128 + (VEC ? h * 128 : 0);
-        // Half h is one block of a weight; a gate/up half holds columns of a gate and of an up block.
-        const float b_lo = VEC ? 1.f : (EPI == F8_EPI_SWIGLU ? cs[0] : cs[h]);
-        const float b_hi = EPI == F8_EPI_SWIGLU ? cs[1] : b_lo;
-        const int buf = (int)(it & 1) * 2 + h;
-        ok = ok && mbar_wait(&tfull[buf], (it >> 1) & 1u, ctl, 2 + q, kWaitAccFull);
-        ok = __all_sync(0xffffffffu, ok);  // tcgen05.ld below needs all 32 lanes converged
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+#pragma unroll 1
+      for (int left = p.k_blocks; left > 0; left -= F8_GROUP, ++groups) {
+        ok = mbar_wait_warp(smem_u32(&sfull[groups & 1]), (groups >> 1) & 1u, p, abort_flag, 2 + q, kWaitFull);
         if (!ok) break;
-        tc_fence_after();
-        // Half 1 is the stage's last product: with it done, both CTAs' operand
-        // tiles have been read and each CTA frees its own stage.
-        if (warp == 8 && lane == 0) mbar_arrive(&empty[stage]);
-        const uint32_t taddr = tmem_base + (uint32_t)(buf * 128) + ((uint32_t)(q * 32) << 16);
-        f8_promote<VEC>(taddr, a_s * b_lo, a_s * b_hi, cs, acc, [&] {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_leader(&tempty[buf]);
-        });
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sempty[sst]);
-        if (++stage == S) stage = 0;
-        if (++sst == F8_SCALE_STAGES) {
-          sst = 0;
-          sphase ^= 1u;
+        const float* sc = sScale + (groups & 1) * GROUP_FLOATS;
+        const float* cs = sc + F8_GROUP * 128 + (VEC ? h * 128 : EPI == F8_EPI_SWIGLU ? 0 : h);
+        sc += q * 32 + lane;
+#pragma unroll 1
+        for (int n = min(left, F8_GROUP); n > 0; --n, ++it) {
+          // Half h is one block of a weight; a gate/up half holds columns of a gate and of an up block.
+          const float lo = VEC ? sc[0] : sc[0] * cs[0];
+          const float hi = EPI == F8_EPI_SWIGLU ? sc[0] * cs[1] : lo;
+          const uint32_t par = it & 1;
+          ok = mbar_wait_warp(tfull_h + par * 16, (it >> 1) & 1u, p, abort_flag, 2 + q, kWaitAccFull);
+          if (!ok) break;
+          tc_fence_after();
+          f8_promote<VEC>(taddr_h + par * 256, lo, hi, cs, acc, [&] {
+            tc_fence_before();
+            __syncwarp();
+            mbar_arrive_leader_if(tempty_h + par * 16, one);
+          });
+          sc += 128;
+          cs += VEC ? 256 : 2;
         }
+        if (!ok) break;
+        __syncwarp();
+        mbar_arrive_if(smem_u32(&sempty[groups & 1]), one);
       }
       if (!ok) break;
-      es.row0 = row0;
       if constexpr (EPI == F8_EPI_BF16) {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + (size_t)row * p.N + col0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (col0 + c * 32 >= p.N) break;
-          uint4 o[4];
+        for (int c = 0; c < 128; c += 16) {
+          if (!rv || col0 + c >= p.N) break;
+          uint32_t w[8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float f[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 v = unpack_f32x2(acc[c * 16 + j * 4 + i]);
-              f[2 * i] = v.x;
-              f[2 * i + 1] = v.y;
-            }
-            o[j] = pack8(f);
-          }
-          es.put(o, &tmO1, col0 + c * 32, false);
+          for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(acc[c + 2 * i], acc[c + 2 * i + 1]);
+          f8_store32(o + c, w, p.wide);
         }
       } else if constexpr (EPI == F8_EPI_F32) {
+        float* o = static_cast<float*>(p.out) + (size_t)row * p.N + col0;
+        if (p.add) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          if (col0 + c * 16 >= p.N) break;
-          uint4 o[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 v = unpack_f32x2(acc[c * 8 + j * 2]), w = unpack_f32x2(acc[c * 8 + j * 2 + 1]);
-            o[j] = make_uint4(__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(w.x), __float_as_uint(w.y));
+          for (int c = 0; c < 128; c += 4) {
+            if (!rv || col0 + c >= p.N) break;
+            f8_add16(o + c, acc + c);
           }
-          es.put(o, &tmO1, col0 + c * 16, p.add != 0);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 128; c += 8) {
+            if (!rv || col0 + c >= p.N) break;
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(acc[c + i]);
+            f8_store32(o + c, w, p.wide);
+          }
         }
       } else {
         // Columns 0-63 are a, 64-127 the same columns of b.  One scale per row
         // and 128 columns: the two halves exchange their maxima.
         float my = 0.f, ma = 0.f, mb = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float2 a = unpack_f32x2(acc[i]), b = unpack_f32x2(acc[32 + i]);
-          my = fmaxf(my, fmaxf(fabsf(a.x * sigmoid_f(a.x) * b.x), fabsf(a.y * sigmoid_f(a.y) * b.y)));
-          ma = fmaxf(ma, fmaxf(fabsf(a.x), fabsf(a.y)));
-          mb = fmaxf(mb, fmaxf(fabsf(b.x), fabsf(b.y)));
+        for (int i = 0; i < 64; ++i) {
+          my = fmaxf(my, fabsf(acc[i] * sigmoid_f(acc[i]) * acc[64 + i]));
+          ma = fmaxf(ma, fabsf(acc[i]));
+          mb = fmaxf(mb, fabsf(acc[64 + i]));
         }
         float* x = sXch + (tiles_done & 1) * 768 + q * 32 + lane;
         x[h * 384] = my;
@@ -552,54 +530,31 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         x[h * 384 + 256] = mb;
         __syncwarp();
         if (lane == 0) mbar_arrive(xch);
-        ok = mbar_wait(xch, tiles_done & 1u, ctl, 2 + q, kWaitAccFull);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = mbar_wait_warp(smem_u32(xch), tiles_done & 1u, p, abort_flag, 2 + q, kWaitAccFull);
         if (!ok) break;
         my = fmaxf(my, x[(h ^ 1) * 384]);
         ma = fmaxf(ma, x[(h ^ 1) * 384 + 128]);
         mb = fmaxf(mb, x[(h ^ 1) * 384 + 256]);
-        if (rv && h == 0) {
-          p.sy[(size_t)n_blk * p.M + row] = fp8_scale<FP8_E4M3>(my);
-          if (p.save_ab) {
-            p.sab[(size_t)n_blk * p.M + row] = fp8_scale<FP8_E4M3>(ma);
-            p.sab[(size_t)(n_blk + p.split / 128) * p.M + row] = fp8_scale<FP8_E4M3>(mb);
-          }
-        }
-        const float fy = fp8_factor<FP8_E4M3>(my);
-        uint4 o[4];
-        auto words = [&](auto value) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 u = value(j * 8 + i * 2), v = value(j * 8 + i * 2 + 1);
-              w[i] = fp8_pack4<FP8_E4M3>(u.x, u.y, v.x, v.y);
+        if (rv) {
+          if (h == 0) {
+            p.sy[(size_t)n_blk * p.M + row] = fp8_scale<FP8_E4M3>(my);
+            if (p.out2 != nullptr) {
+              p.sab[(size_t)n_blk * p.M + row] = fp8_scale<FP8_E4M3>(ma);
+              p.sab[(size_t)(n_blk + p.split / 128) * p.M + row] = fp8_scale<FP8_E4M3>(mb);
             }
-            o[j] = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        };
-        words([&](int i) {
-          const float2 a = unpack_f32x2(acc[i]), b = unpack_f32x2(acc[32 + i]);
-          return make_float2(a.x * sigmoid_f(a.x) * b.x * fy, a.y * sigmoid_f(a.y) * b.y * fy);
-        });
-        es.put(o, &tmO1, col0, false);
-        if (p.save_ab) {
-          const float fa = fp8_factor<FP8_E4M3>(ma), fb = fp8_factor<FP8_E4M3>(mb);
-          words([&](int i) {
-            const float2 a = unpack_f32x2(acc[i]);
-            return make_float2(a.x * fa, a.y * fa);
-          });
-          es.put(o, &tmO2, col0, false);
-          words([&](int i) {
-            const float2 b = unpack_f32x2(acc[32 + i]);
-            return make_float2(b.x * fb, b.y * fb);
-          });
-          es.put(o, &tmO2, p.split + col0, false);
+          const float fy = fp8_factor<FP8_E4M3>(my);
+          f8_store_row64(static_cast<uint8_t*>(p.out) + (size_t)row * p.N + col0, p.wide,
+                         [&](int i) { return acc[i] * sigmoid_f(acc[i]) * acc[64 + i] * fy; });
+          if (p.out2 != nullptr) {
+            const float fa = fp8_factor<FP8_E4M3>(ma), fb = fp8_factor<FP8_E4M3>(mb);
+            uint8_t* ab = static_cast<uint8_t*>(p.out2) + (size_t)row * 2 * p.N + col0;
+            f8_store_row64(ab, p.wide, [&](int i) { return acc[i] * fa; });
+            f8_store_row64(ab + p.split, p.wide, [&](int i) { return acc[64 + i] * fb; });
+          }
         }
       }
     }
-    es.finish();
   }
 
   tc_fence_before();
