@@ -148,25 +148,32 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// mbar_wait for a converged warp on a barrier that is about to complete: polled
-// in a tight loop (a poll sleeps in hardware until the phase ends or some
-// microseconds have passed), the bounded wait behind it.  Uniform result.
-template <typename Params>
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, const Params& prm,
-                                               volatile int* abort_flag, uint32_t role, uint32_t reason) {
-  uint32_t ok;
+// Control words of the drain's waits, in shared memory: the abort flag (nonzero:
+// some role gave up; the detail word's role and reason, or 1 when mbar_wait has
+// recorded it) and the limit.
+struct DrainCtl {
+  uint32_t abort;
+  uint32_t unused;
+  uint64_t limit_ns;
+};
+
+// Bounded wait of a whole warp on a barrier that is about to complete.  The
+// drain is latency-bound, so success costs a poll and a branch: there is no
+// result.  A wait that runs out, or sees that another role has given up, sets or
+// leaves the abort flag and returns; the caller looks at the flag every few
+// blocks and what it computed since then is not stored.
+__device__ __forceinline__ void mbar_wait_drain(uint32_t bar, uint32_t parity, uint32_t ctl, uint32_t detail) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
-      "POLL:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
-      "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 16;\n\t@q bra POLL;\n"
-      "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      "{\n\t.reg .pred p;\n\t.reg .u32 f;\n\t.reg .u64 t0, t1, lim;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t@p bra DONE;\n\t"
+      "mov.u64 t0, %%globaltimer;\n\tld.shared.u64 lim, [%2 + 8];\n"
+      "POLL:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t@p bra DONE;\n\t"
+      "ld.volatile.shared.u32 f, [%2];\n\tsetp.ne.u32 p, f, 0;\n\t@p bra DONE;\n\t"
+      "mov.u64 t1, %%globaltimer;\n\tsub.u64 t1, t1, t0;\n\tsetp.lt.u64 p, t1, lim;\n\t@p bra POLL;\n\t"
+      "st.volatile.shared.u32 [%2], %3;\n"
+      "DONE:\n\t}\n" ::"r"(bar),
+      "r"(parity), "r"(ctl), "r"(detail)
       : "memory");
-  if (__all_sync(0xffffffffu, ok != 0)) return true;
-  const WaitCtl c{abort_flag, prm.status, prm.wait_limit_ns, prm.kernel_id};
-  return __all_sync(0xffffffffu,
-                    mbar_wait(static_cast<uint64_t*>(__cvta_shared_to_generic(bar)), parity, c, role, reason));
 }
 // Arrive where `pred` is set, without a branch.
 __device__ __forceinline__ void mbar_arrive_if(uint32_t bar, uint32_t pred) {
@@ -270,7 +277,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   uint64_t* sempty = sfull + 2;
   uint64_t* mma_done = sempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  DrainCtl* drain_ctl = reinterpret_cast<DrainCtl*>(
+      (reinterpret_cast<uintptr_t>(tmem_slot + 1) + 15) & ~static_cast<uintptr_t>(15));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(&drain_ctl->abort);
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0);  // known uniform
   const int lane = threadIdx.x % 32;
@@ -294,6 +303,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
+    drain_ctl->limit_ns = p.wait_limit_ns;
     fence_mbar_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
@@ -404,7 +414,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         const int nb = EPI == F8_EPI_SWIGLU ? n_blk + lane * (p.split / 128) : n_blk * 2 + lane;
         const bool sbv = EPI == F8_EPI_SWIGLU || nb * 128 < p.N;
         for (int kb0 = 0; kb0 < p.k_blocks; kb0 += F8_GROUP) {
-          ok = mbar_wait_warp(smem_u32(&sempty[st]), phase ^ 1u, p, abort_flag, 6, kWaitEmpty);
+          ok = __all_sync(0xffffffffu, mbar_wait(&sempty[st], phase ^ 1u, ctl, 6, kWaitEmpty));
           if (!ok) break;
           float* dst = sScale + st * GROUP_FLOATS;
           float* dst_b = dst + F8_GROUP * 128;
@@ -442,11 +452,12 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     const int q = warp & 3;           // TMEM lane quarter this warp may access
     const int h = (warp - 4) / 4;     // column half
     const uint32_t one = lane == 0;  // this warp's arrivals
-    const uint32_t tfull_h = smem_u32(&tfull[h]);
-    const uint32_t tempty_h = mapa_shared(smem_u32(&tempty[h]), 0);
-    const uint32_t taddr_h = tmem_base + (uint32_t)(h * 128) + ((uint32_t)(q * 32) << 16);
+    const uint32_t wctl = smem_u32(drain_ctl);
+    // Buffers of parity 0; parity 1 is 16 bytes and 256 columns on (bits that are 0 here).
+    uint32_t tfull_h = smem_u32(&tfull[h]);
+    uint32_t tempty_h = mapa_shared(smem_u32(&tempty[h]), 0);
+    uint32_t taddr_h = tmem_base + (uint32_t)(h * 128) + ((uint32_t)(q * 32) << 16);
     uint32_t it = 0, groups = 0, tiles_done = 0;
-    bool ok = true;
     for (int tile = first_tile; tile < num_tiles; tile += tile_step, ++tiles_done) {
       int m_blk, n_blk;
       tile_coords(tile, p.num_m_tiles, p.num_n_tiles, p.group_m, m_blk, n_blk);
@@ -459,8 +470,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
 #pragma unroll 1
       for (int left = p.k_blocks; left > 0; left -= F8_GROUP, ++groups) {
-        ok = mbar_wait_warp(smem_u32(&sfull[groups & 1]), (groups >> 1) & 1u, p, abort_flag, 2 + q, kWaitFull);
-        if (!ok) break;
+        mbar_wait_drain(smem_u32(&sfull[groups & 1]), (groups >> 1) & 1u, wctl, (2 + q) << 8 | kWaitFull);
+        if (*abort_flag) break;
         const float* sc = sScale + (groups & 1) * GROUP_FLOATS;
         const float* cs = sc + F8_GROUP * 128 + (VEC ? h * 128 : EPI == F8_EPI_SWIGLU ? 0 : h);
         sc += q * 32 + lane;
@@ -469,23 +480,23 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
           // Half h is one block of a weight; a gate/up half holds columns of a gate and of an up block.
           const float lo = VEC ? sc[0] : sc[0] * cs[0];
           const float hi = EPI == F8_EPI_SWIGLU ? sc[0] * cs[1] : lo;
-          const uint32_t par = it & 1;
-          ok = mbar_wait_warp(tfull_h + par * 16, (it >> 1) & 1u, p, abort_flag, 2 + q, kWaitAccFull);
-          if (!ok) break;
+          mbar_wait_drain(tfull_h, (it >> 1) & 1u, wctl, (2 + q) << 8 | kWaitAccFull);
           tc_fence_after();
-          f8_promote<VEC>(taddr_h + par * 256, lo, hi, cs, acc, [&] {
+          f8_promote<VEC>(taddr_h, lo, hi, cs, acc, [&] {
             tc_fence_before();
             __syncwarp();
-            mbar_arrive_leader_if(tempty_h + par * 16, one);
+            mbar_arrive_leader_if(tempty_h, one);
           });
+          tfull_h ^= 16;
+          tempty_h ^= 16;
+          taddr_h ^= 256;
           sc += 128;
           cs += VEC ? 256 : 2;
         }
-        if (!ok) break;
         __syncwarp();
         mbar_arrive_if(smem_u32(&sempty[groups & 1]), one);
       }
-      if (!ok) break;
+      if (__any_sync(0xffffffffu, *abort_flag)) break;  // some block above may not have been complete
       if constexpr (EPI == F8_EPI_BF16) {
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + (size_t)row * p.N + col0;
 #pragma unroll
@@ -530,8 +541,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         x[h * 384 + 256] = mb;
         __syncwarp();
         if (lane == 0) mbar_arrive(xch);
-        ok = mbar_wait_warp(smem_u32(xch), tiles_done & 1u, p, abort_flag, 2 + q, kWaitAccFull);
-        if (!ok) break;
+        mbar_wait_drain(smem_u32(xch), tiles_done & 1u, wctl, (2 + q) << 8 | kWaitAccFull);
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
         my = fmaxf(my, x[(h ^ 1) * 384]);
         ma = fmaxf(ma, x[(h ^ 1) * 384 + 128]);
         mb = fmaxf(mb, x[(h ^ 1) * 384 + 256]);
@@ -560,6 +571,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   tc_fence_before();
   cluster_sync();
   if (*abort_flag) {
+    if (threadIdx.x == 0 && *abort_flag != 1 && p.status != nullptr) {  // a drain warp's wait
+      atomicCAS(p.status, 0u, 7u /* CODA_ERR_DEVICE_TIMEOUT */);
+      atomicCAS(p.status + 1, 0u, (p.kernel_id << 16) | (uint32_t)*abort_flag);
+    }
     // A role gave up: let the last (up to STAGES) copies land before shared
     // memory is released.  Every wait here is bounded too.
     if (warp == 0 && lane == 0 && rank == 0) {
