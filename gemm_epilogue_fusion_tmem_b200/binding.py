@@ -698,19 +698,32 @@ def _req2(t, name: str) -> tuple:
     return tuple(t.shape)
 
 
-def _same_device(dev, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+def _in(t, name: str, dtype, shape, dev=None):
+    """The device address of an argument, after _req's checks; it must lie on `dev`."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape
+            and t.is_contiguous()):
+        _req(t, name, dtype, shape)  # says what is wrong
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+    return t.data_ptr()
 
 
-def _give(o: dict, key: str, shape, dtype, dev) -> torch.Tensor:
-    """The caller's output tensor o[key], checked, or a new one."""
-    if key not in o:
-        o[key] = torch.empty(shape, dtype=dtype, device=dev)
-    _req(o[key], key, dtype, shape)
-    _same_device(dev, **{key: o[key]})
-    return o[key]
+def _out(o: dict, key: str, shape, dtype, dev):
+    """The device address of the caller's output o[key], checked, or of a new one."""
+    t = o.get(key)
+    if t is None:
+        t = o[key] = torch.empty(shape, dtype=dtype, device=dev)
+        return t.data_ptr()
+    return _in(t, key, dtype, shape, dev)
+
+
+def _call(name: str, dev, *args) -> None:
+    """Call an entry point on `dev`'s current stream (the device need not be the current one)."""
+    if torch.cuda.current_device() == dev.index:
+        _check(getattr(_lib, name)(*args, torch._C._cuda_getCurrentRawStream(dev.index)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(getattr(_lib, name)(*args, torch._C._cuda_getCurrentRawStream(dev.index)), name)
 
 
 _status_ws: dict = {}
@@ -745,42 +758,35 @@ def quant_fp8(X, rows: bool = True, cols: bool = False, rowvec=None, colvec=None
 
     rows: Qr [R, C], Sr [ceil(C/128), R], one scale per row and 128 columns;
     cols: Qc [R, C], Sc [ceil(R/128), C], one scale per column and 128 rows."""
+    library()
     R, C = _req2(X, "X")
-    _req(X, "X")
+    x = _in(X, "X", torch.bfloat16, (R, C))
     f = _fp8(fmt, "fmt")
     if not rows and not cols:
         raise ValueError("rows or cols (or both) must be asked for")
-    if rowvec is not None:
-        _req(rowvec, "rowvec", torch.float32, (R,))
-    if colvec is not None:
-        _req(colvec, "colvec", shape=(C,))
     dev = X.device
-    _same_device(dev, rowvec=rowvec, colvec=colvec)
+    rv = None if rowvec is None else _in(rowvec, "rowvec", torch.float32, (R,), dev)
+    cv = None if colvec is None else _in(colvec, "colvec", torch.bfloat16, (C,), dev)
     o = dict(out or {})
+    qr = sr = qc = sc = None
     if rows:
-        _give(o, "Qr", (R, C), fmt, dev), _give(o, "Sr", (_cdiv(C, 128), R), torch.float32, dev)
+        qr, sr = _out(o, "Qr", (R, C), fmt, dev), _out(o, "Sr", (_cdiv(C, 128), R), torch.float32, dev)
     if cols:
-        _give(o, "Qc", (R, C), fmt, dev), _give(o, "Sc", (_cdiv(R, 128), C), torch.float32, dev)
-    with torch.cuda.device(dev):
-        _check(library().coda_quant_fp8(_ptr(X), _ptr(rowvec), _ptr(colvec),
-                                        _ptr(o["Qr"] if rows else None), _ptr(o["Sr"] if rows else None),
-                                        _ptr(o["Qc"] if cols else None), _ptr(o["Sc"] if cols else None),
-                                        R, C, f, _stream()), "coda_quant_fp8")
+        qc, sc = _out(o, "Qc", (R, C), fmt, dev), _out(o, "Sc", (_cdiv(R, 128), C), torch.float32, dev)
+    _call("coda_quant_fp8", dev, x, rv, cv, qr, sr, qc, sc, R, C, f)
     return o
 
 
 def quant_fp8_blocks(W, fmt=torch.float8_e4m3fn, out: dict | None = None) -> dict:
     """A weight W (bf16 [R, C]) in 8 bits with a scale per 128 x 128 block: Q, S
     [ceil(R/128), ceil(C/128)]; see coda_quant_fp8_blocks."""
+    library()
     R, C = _req2(W, "W")
-    _req(W, "W")
+    w = _in(W, "W", torch.bfloat16, (R, C))
     f = _fp8(fmt, "fmt")
-    dev = W.device
     o = dict(out or {})
-    _give(o, "Q", (R, C), fmt, dev), _give(o, "S", (_cdiv(R, 128), _cdiv(C, 128)), torch.float32, dev)
-    with torch.cuda.device(dev):
-        _check(library().coda_quant_fp8_blocks(_ptr(W), _ptr(o["Q"]), _ptr(o["S"]), R, C, f, _stream()),
-               "coda_quant_fp8_blocks")
+    _call("coda_quant_fp8_blocks", W.device, w, _out(o, "Q", (R, C), fmt, W.device),
+          _out(o, "S", (_cdiv(R, 128), _cdiv(C, 128)), torch.float32, W.device), R, C, f)
     return o
 
 
@@ -794,29 +800,25 @@ def gemm_fp8(A, SA, B, SB, M: int, N: int, K: int, a_mn_major: bool = False, b_m
     B as stored, or (b_blocks=False) [ceil(K/128), N].  out_dtype bf16 or fp32;
     accumulate adds to an fp32 `out`.  Without `ws`, fp8_status() reads the
     status word."""
-    lib = library()
+    library()
     if not all(isinstance(t, torch.Tensor) for t in (A, SA, B, SB)):
         raise TypeError("A, SA, B and SB must be torch.Tensors")
     fa, fb = _fp8(A.dtype, "A"), _fp8(B.dtype, "B")
-    _req(A, "A", A.dtype, (K, M) if a_mn_major else (M, K))
-    _req(B, "B", B.dtype, (K, N) if b_mn_major else (N, K))
-    kb = _cdiv(K, 128)
-    _req(SA, "SA", torch.float32, (kb, M))
-    nb = _cdiv(N, 128)
-    _req(SB, "SB", torch.float32, ((kb, nb) if b_mn_major else (nb, kb)) if b_blocks else (kb, N))
+    dev = A.device
+    kb, nb = _cdiv(K, 128), _cdiv(N, 128)
+    a = _in(A, "A", A.dtype, (K, M) if a_mn_major else (M, K))
+    b = _in(B, "B", B.dtype, (K, N) if b_mn_major else (N, K), dev)
+    sa = _in(SA, "SA", torch.float32, (kb, M), dev)
+    sb = _in(SB, "SB", torch.float32, ((kb, nb) if b_mn_major else (nb, kb)) if b_blocks else (kb, N), dev)
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
     if accumulate and (out is None or out_dtype != torch.float32):
         raise ValueError("accumulate adds to an fp32 `out`: give one, with out_dtype=torch.float32")
-    dev = A.device
-    C = out if out is not None else torch.empty(M, N, dtype=out_dtype, device=dev)
-    _req(C, "C", out_dtype, (M, N))
-    _same_device(dev, SA=SA, B=B, SB=SB, C=C)
-    with torch.cuda.device(dev):
-        ws = ws or _status_workspace(dev)
-        _check(lib.coda_gemm_fp8(_ptr(A), _ptr(SA), _ptr(B), _ptr(SB), _ptr(C), M, N, K, int(a_mn_major),
-                                 int(b_mn_major), fa, fb, int(b_blocks), int(out_dtype == torch.float32),
-                                 int(accumulate), ws.ptr(), ws.nbytes, _stream()), "coda_gemm_fp8")
+    C = out if out is not None else torch.empty((M, N), dtype=out_dtype, device=dev)
+    c = _in(C, "C", out_dtype, (M, N), dev)
+    ws = ws or _status_workspace(dev)
+    _call("coda_gemm_fp8", dev, a, sa, b, sb, c, M, N, K, int(a_mn_major), int(b_mn_major), fa, fb, int(b_blocks),
+          int(out_dtype == torch.float32), int(accumulate), ws.buf.data_ptr(), ws.nbytes)
     return C
 
 
@@ -825,28 +827,24 @@ def gemm_swiglu_fp8(A, SA, Wgu, SW, save_ab: bool = True, out: dict | None = Non
     """Gate/up product with SwiGLU on 8-bit operands (e4m3): Y [M, F] with SY
     [F/128, M] and, with save_ab, the checkpoint AB = [a | b] [M, 2F] with SAB
     [2F/128, M]; see coda_gemm_swiglu_fp8."""
-    lib = library()
+    library()
     e4m3 = torch.float8_e4m3fn
     M, K = _req2(A, "A")
     F = _req2(Wgu, "Wgu")[0] // 2
-    _req(A, "A", e4m3), _req(Wgu, "Wgu", e4m3, (2 * F, K))
-    kb = _cdiv(K, 128)
-    _req(SA, "SA", torch.float32, (kb, M))
+    dev = A.device
+    kb, fb = _cdiv(K, 128), F // 128
+    a = _in(A, "A", e4m3, (M, K))
+    w = _in(Wgu, "Wgu", e4m3, (2 * F, K), dev)
     if F % 128 != 0:
         raise CodaError(2, "coda_gemm_swiglu_fp8")
-    fb = F // 128
-    _req(SW, "SW", torch.float32, (2 * fb, kb))
-    dev = A.device
-    _same_device(dev, SA=SA, Wgu=Wgu, SW=SW)
+    sa, sw = _in(SA, "SA", torch.float32, (kb, M), dev), _in(SW, "SW", torch.float32, (2 * fb, kb), dev)
     o = dict(out or {})
-    _give(o, "Y", (M, F), e4m3, dev), _give(o, "SY", (fb, M), torch.float32, dev)
+    y, sy = _out(o, "Y", (M, F), e4m3, dev), _out(o, "SY", (fb, M), torch.float32, dev)
+    ab = sab = None
     if save_ab:
-        _give(o, "AB", (M, 2 * F), e4m3, dev), _give(o, "SAB", (2 * fb, M), torch.float32, dev)
-    with torch.cuda.device(dev):
-        ws = ws or _status_workspace(dev)
-        _check(lib.coda_gemm_swiglu_fp8(_ptr(A), _ptr(SA), _ptr(Wgu), _ptr(SW), _ptr(o["Y"]), _ptr(o["SY"]),
-                                        _ptr(o["AB"] if save_ab else None), _ptr(o["SAB"] if save_ab else None),
-                                        M, K, F, ws.ptr(), ws.nbytes, _stream()), "coda_gemm_swiglu_fp8")
+        ab, sab = _out(o, "AB", (M, 2 * F), e4m3, dev), _out(o, "SAB", (2 * fb, M), torch.float32, dev)
+    ws = ws or _status_workspace(dev)
+    _call("coda_gemm_swiglu_fp8", dev, a, sa, w, sw, y, sy, ab, sab, M, K, F, ws.buf.data_ptr(), ws.nbytes)
     return o
 
 
@@ -854,26 +852,24 @@ def swiglu_fp8_bwd(dY, AB, SAB, cols: bool = True, fmt=torch.float8_e4m3fn, out:
     """SwiGLU backward from the 8-bit checkpoint: dA = [da | db] (rows form, SdA)
     and, with cols, dAc, SdAc and Yc, SYc (columns form, the operands of the
     weight gradients); see coda_swiglu_fp8_bwd.  fmt is dA's and dAc's type."""
+    library()
     e4m3 = torch.float8_e4m3fn
     M, F = _req2(dY, "dY")
-    _req(dY, "dY")
-    _req(AB, "AB", e4m3, (M, 2 * F))
+    dev = dY.device
+    fb, mb = F // 128, _cdiv(M, 128)
+    dy = _in(dY, "dY", torch.bfloat16, (M, F))
+    ab = _in(AB, "AB", e4m3, (M, 2 * F), dev)
     f = _fp8(fmt, "fmt")
     if F % 128 != 0:
         raise CodaError(2, "coda_swiglu_fp8_bwd")
-    fb, mb = F // 128, _cdiv(M, 128)
-    _req(SAB, "SAB", torch.float32, (2 * fb, M))
-    dev = dY.device
-    _same_device(dev, AB=AB, SAB=SAB)
+    sab = _in(SAB, "SAB", torch.float32, (2 * fb, M), dev)
     o = dict(out or {})
-    _give(o, "dA", (M, 2 * F), fmt, dev), _give(o, "SdA", (2 * fb, M), torch.float32, dev)
+    da, sda = _out(o, "dA", (M, 2 * F), fmt, dev), _out(o, "SdA", (2 * fb, M), torch.float32, dev)
+    dac = sdac = yc = syc = None
     if cols:
-        _give(o, "dAc", (M, 2 * F), fmt, dev), _give(o, "SdAc", (mb, 2 * F), torch.float32, dev)
-        _give(o, "Yc", (M, F), e4m3, dev), _give(o, "SYc", (mb, F), torch.float32, dev)
-    c = [_ptr(o[k] if cols else None) for k in ("dAc", "SdAc", "Yc", "SYc")]
-    with torch.cuda.device(dev):
-        _check(library().coda_swiglu_fp8_bwd(_ptr(dY), _ptr(AB), _ptr(SAB), _ptr(o["dA"]), _ptr(o["SdA"]), *c,
-                                             M, F, f, _stream()), "coda_swiglu_fp8_bwd")
+        dac, sdac = _out(o, "dAc", (M, 2 * F), fmt, dev), _out(o, "SdAc", (mb, 2 * F), torch.float32, dev)
+        yc, syc = _out(o, "Yc", (M, F), e4m3, dev), _out(o, "SYc", (mb, F), torch.float32, dev)
+    _call("coda_swiglu_fp8_bwd", dev, dy, ab, sab, da, sda, dac, sdac, yc, syc, M, F, f)
     return o
 
 
@@ -881,21 +877,17 @@ def rmsnorm_fp8_fwd(X, g, eps: float, R=None, out: dict | None = None) -> dict:
     """H = X + R (when R is given), r = rsqrt(mean H^2 + eps), and H r g in 8
     bits: Q [M, d] e4m3, S [ceil(d/128), M]; returns H (with R), r, Q, S; see
     coda_rmsnorm_fp8_fwd."""
+    library()
     M, d = _req2(X, "X")
-    _req(X, "X"), _req(g, "g", shape=(d,))
-    if R is not None:
-        _req(R, "R", shape=(M, d))
     dev = X.device
-    _same_device(dev, g=g, R=R)
+    x, gp = _in(X, "X", torch.bfloat16, (M, d)), _in(g, "g", torch.bfloat16, (d,), dev)
     o = dict(out or {})
+    rp = hp = None
     if R is not None:
-        _give(o, "H", (M, d), torch.bfloat16, dev)
-    _give(o, "r", (M,), torch.float32, dev)
-    _give(o, "Q", (M, d), torch.float8_e4m3fn, dev), _give(o, "S", (_cdiv(d, 128), M), torch.float32, dev)
-    with torch.cuda.device(dev):
-        _check(library().coda_rmsnorm_fp8_fwd(_ptr(X), _ptr(R), _ptr(g), _ptr(o["H"] if R is not None else None),
-                                              _ptr(o["r"]), _ptr(o["Q"]), _ptr(o["S"]), M, d, float(eps), _stream()),
-               "coda_rmsnorm_fp8_fwd")
+        rp, hp = _in(R, "R", torch.bfloat16, (M, d), dev), _out(o, "H", (M, d), torch.bfloat16, dev)
+    _call("coda_rmsnorm_fp8_fwd", dev, x, rp, gp, hp, _out(o, "r", (M,), torch.float32, dev),
+          _out(o, "Q", (M, d), torch.float8_e4m3fn, dev), _out(o, "S", (_cdiv(d, 128), M), torch.float32, dev),
+          M, d, float(eps))
     return o
 
 
@@ -904,20 +896,15 @@ def rmsnorm_fp8_bwd(dN, H, r, g, dH_in=None, out: dict | None = None, ws: Worksp
     through): returns dH (bf16, the gradient of X and of R) and dg (fp32); see
     coda_rmsnorm_fp8_bwd.  Without `ws` the scratch is this call's own."""
     lib = library()
+    bf16 = torch.bfloat16
     M, d = _req2(dN, "dN")
-    _req(dN, "dN"), _req(H, "H", shape=(M, d)), _req(r, "r", torch.float32, (M,)), _req(g, "g", shape=(d,))
-    if dH_in is not None:
-        _req(dH_in, "dH_in", shape=(M, d))
     dev = dN.device
-    _same_device(dev, H=H, r=r, g=g, dH_in=dH_in)
+    dn, h = _in(dN, "dN", bf16, (M, d)), _in(H, "H", bf16, (M, d), dev)
+    rp, gp = _in(r, "r", torch.float32, (M,), dev), _in(g, "g", bf16, (d,), dev)
+    hi = None if dH_in is None else _in(dH_in, "dH_in", bf16, (M, d), dev)
     o = dict(out or {})
-    _give(o, "dH", (M, d), torch.bfloat16, dev), _give(o, "dg", (d,), torch.float32, dev)
-    with torch.cuda.device(dev):
-        if ws is None:
-            buf = torch.empty(lib.coda_rmsnorm_fp8_bwd_workspace_bytes(M, d), dtype=torch.uint8, device=dev)
-            wp, wn = ctypes.c_void_p(buf.data_ptr()), buf.numel()
-        else:
-            wp, wn = ws.ptr(), ws.nbytes
-        _check(lib.coda_rmsnorm_fp8_bwd(_ptr(dN), _ptr(H), _ptr(r), _ptr(g), _ptr(dH_in), _ptr(o["dH"]),
-                                        _ptr(o["dg"]), M, d, wp, wn, _stream()), "coda_rmsnorm_fp8_bwd")
+    dh, dg = _out(o, "dH", (M, d), bf16, dev), _out(o, "dg", (d,), torch.float32, dev)
+    buf = ws.buf if ws is not None else torch.empty(lib.coda_rmsnorm_fp8_bwd_workspace_bytes(M, d), dtype=torch.uint8,
+                                                    device=dev)
+    _call("coda_rmsnorm_fp8_bwd", dev, dn, h, rp, gp, hi, dh, dg, M, d, buf.data_ptr(), buf.numel())
     return o

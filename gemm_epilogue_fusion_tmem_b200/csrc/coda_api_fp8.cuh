@@ -66,6 +66,17 @@ bool operand8_map_b(CUtensorMap* m, const void* p, long long mn, long long k, bo
   return make_tmap8(m, p, mn, k, F8_BK, 64, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+bool operand8_map_k(CUtensorMap* m, const void* p, long long mn, long long k, int box_mn) {
+  return make_tmap8(m, p, mn, k, F8_BK, box_mn, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Few rows of A: the weight becomes the MMA's 128-row operand, the rows its
+// columns (gemm_fp8_skinny_kernel).  Measured at N = K = 4096: 16 rows 6.9 us,
+// 64 rows 9.5 us, where a 256 x 256 tile is mostly padding (17 us); at 128 rows
+// the other way round (30 us).  The gate/up product holds two accumulators and
+// changes over at half the rows (64 rows, K = 4096, F = 11008: 69 us against 35).
+inline int skinny8_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
+
 // Rasterisation as pick_group, in bytes of 8-bit operands.
 int pick_group8(long long a_rows, long long b_rows, int num_m, int num_n, int k_blocks, int clusters) {
   int side = 1;
@@ -122,6 +133,35 @@ coda_status launch_gemm8_majors(const CUtensorMap& ta, const CUtensorMap& tb, bo
   if (!a_mn && b_mn) return launch_gemm8<EPI, false, true, VEC>(ta, tb, p, s);
   if (a_mn && b_mn) return launch_gemm8<EPI, true, true, VEC>(ta, tb, p, s);
   return launch_gemm8<EPI, true, false, VEC>(ta, tb, p, s);
+}
+
+// Tiles of the few-rows kernel: 128 weight rows (and their partners in the up
+// half) x TN rows of A, split over k by a cluster.
+template <int TN, bool SWIGLU>
+coda_status launch_skinny8(const CUtensorMap& tw, const CUtensorMap& tx, Skinny8Params p, cudaStream_t s) {
+  using C = F8SkinnyCfg<TN, SWIGLU>;
+  static std::atomic<bool> ready[kMaxDevices];
+  int dev = 0;
+  coda_status st = current_device(dev);
+  if (st != CODA_OK) return st;
+  auto kern = gemm_fp8_skinny_kernel<TN, SWIGLU>;
+  if (!ready[dev].load()) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
+      return CODA_ERR_CUDA;
+    ready[dev].store(true);
+  }
+  p.num_m_tiles = cdiv(p.M, TN);
+  const int tiles = cdiv(p.N, 128) * p.num_m_tiles;
+  int splits = 1;
+  while (splits < 8 && tiles * splits * 2 <= 2 * g_dev[dev].num_sms && splits * 4 <= p.k_blocks) splits *= 2;
+  p.idesc = (p.idesc & ~(0x3Fu << 17)) | ((uint32_t)(TN >> 3) << 17);
+  p.wait_limit_ns = g_wait_limit_ns.load();
+  p.kernel_id = 0x60 + (uint32_t)(TN / 16 * 2 + (SWIGLU ? 1 : 0));
+  g_launch_tag = SWIGLU ? CODA_KERNEL_GEMM_SWIGLU_FP8 : CODA_KERNEL_GEMM_FP8;
+  const cudaError_t e =
+      launch_ex(kern, dim3(tiles * splits), dim3(F8S_THREADS), C::SMEM_BYTES, s, splits, tw, tx, p);
+  g_launch_tag = -1;
+  return e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess ? CODA_OK : CODA_ERR_CUDA;
 }
 
 inline bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
@@ -254,7 +294,28 @@ coda_status coda_gemm_fp8(const void* A, const float* SA, const void* B, const f
   int dev;
   CODA_TRY(current_device(dev));
   const bool a_mn = a_mn_major != 0, b_mn = b_mn_major != 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   CUtensorMap ta, tb;
+  if (M <= 64 && !a_mn && !b_mn && b_blocks) {
+    const int tn = skinny8_rows(M);
+    if (!operand8_map_k(&tb, B, N, K, 128) || !operand8_map_k(&ta, A, M, K, tn)) return CODA_ERR_CUDA;
+    Skinny8Params p;
+    std::memset(&p, 0, sizeof(p));
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.k_blocks = cdiv(K, F8_BK);
+    p.sa = SA;
+    p.sb = SB;
+    p.c_fp32 = c_fp32;
+    p.add = accumulate;
+    p.out = C;
+    p.idesc = make_idesc_f8(128, 0, b_format, a_format, false, false);  // the weight is the MMA's first operand
+    p.status = static_cast<uint32_t*>(ws);
+    if (tn == 16) return launch_skinny8<16, false>(tb, ta, p, s);
+    if (tn == 32) return launch_skinny8<32, false>(tb, ta, p, s);
+    return launch_skinny8<64, false>(tb, ta, p, s);
+  }
   if (!operand8_map_a(&ta, A, M, K, a_mn) || !operand8_map_b(&tb, B, N, K, b_mn)) return CODA_ERR_CUDA;
   Gemm8Params p;
   std::memset(&p, 0, sizeof(p));
@@ -275,7 +336,6 @@ coda_status coda_gemm_fp8(const void* A, const float* SA, const void* B, const f
   p.wide = aligned32(C);
   p.idesc = make_idesc_f8(256, 128, a_format, b_format, a_mn, b_mn);
   p.status = static_cast<uint32_t*>(ws);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (c_fp32)
     return b_blocks ? launch_gemm8_majors<F8_EPI_F32, false>(ta, tb, a_mn, b_mn, p, s)
                     : launch_gemm8_majors<F8_EPI_F32, true>(ta, tb, a_mn, b_mn, p, s);
@@ -299,6 +359,28 @@ coda_status coda_gemm_swiglu_fp8(const void* A, const float* SA, const void* Wgu
   int dev;
   CODA_TRY(current_device(dev));
   CUtensorMap ta, tb;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M <= 32) {
+    const int tn = skinny8_rows(M);
+    if (!operand8_map_k(&tb, Wgu, 2LL * F, K, 128) || !operand8_map_k(&ta, A, M, K, tn)) return CODA_ERR_CUDA;
+    Skinny8Params p;
+    std::memset(&p, 0, sizeof(p));
+    p.M = M;
+    p.N = F;
+    p.K = K;
+    p.k_blocks = cdiv(K, F8_BK);
+    p.sa = SA;
+    p.sb = SW;
+    p.split = F;
+    p.out = Y;
+    p.out2 = static_cast<uint8_t*>(AB_or_null);
+    p.sy = SY;
+    p.sab = SAB_or_null;
+    p.idesc = make_idesc_f8(128, 0, FP8_E4M3, FP8_E4M3, false, false);
+    p.status = static_cast<uint32_t*>(ws);
+    if (tn == 16) return launch_skinny8<16, true>(tb, ta, p, s);
+    return launch_skinny8<32, true>(tb, ta, p, s);
+  }
   if (!operand8_map_a(&ta, A, M, K, false) || !operand8_map_b(&tb, Wgu, 2LL * F, K, false)) return CODA_ERR_CUDA;
   Gemm8Params p;
   std::memset(&p, 0, sizeof(p));
@@ -321,7 +403,7 @@ coda_status coda_gemm_swiglu_fp8(const void* A, const float* SA, const void* Wgu
   p.sab = SAB_or_null;
   p.idesc = make_idesc_f8(256, 128, FP8_E4M3, FP8_E4M3, false, false);
   p.status = static_cast<uint32_t*>(ws);
-  return launch_gemm8<F8_EPI_SWIGLU, false, false, false>(ta, tb, p, static_cast<cudaStream_t>(stream));
+  return launch_gemm8<F8_EPI_SWIGLU, false, false, false>(ta, tb, p, s);
 }
 
 // ------------------------------------------------------------------ SwiGLU backward

@@ -615,4 +615,371 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   }
 }
 
+// ------------------------------------------------------------------ few rows
+//
+// C[m, n] for few rows m (decoding steps, short prompts): the weight is the
+// MMA's 128-row operand and the rows of A, TN of them, are its columns, so no
+// MMA row is padding.  The product is then a stream of the weight, and the k
+// axis is split over a cluster of up to 8 CTAs so that about two CTAs per SM
+// have loads in flight; their fp32 partial tiles are added through distributed
+// shared memory, in rank order, each CTA finishing its share of the rows.
+// Roles (192 threads): warp 0 TMA producer, warp 1 TMEM owner and MMA issuer,
+// warps 2-5 one weight row per thread.
+constexpr int F8S_THREADS = 192;
+
+template <int TN, bool SWIGLU>
+struct F8SkinnyCfg {
+  static constexpr int W = SWIGLU ? 2 : 1;  // products per tile: gate and up
+  static constexpr int STAGE_BYTES = W * F8_A_BYTES + TN * F8_BK;
+  static constexpr int STAGES = SWIGLU ? (TN == 16 ? 3 : 2) : TN <= 32 ? 5 : TN == 64 ? 4 : 3;
+  static constexpr int CHUNK = 1024 / W;  // scales staged at a time, per product
+  static constexpr int BUFS = TN * W <= 64 ? 4 : 256 / (TN * W);  // TMEM buffers
+  static constexpr uint32_t TMEM = BUFS * TN * W < 32 ? 32 : BUFS * TN * W;
+  static constexpr int SCALE_BYTES = 2 * W * CHUNK * 4;
+  // Row maxima of the 8-bit outputs: [TN][3][4 warps].
+  static constexpr int MAX_BYTES = SWIGLU ? TN * 12 * 4 : 0;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SCALE_BYTES + MAX_BYTES + 1024 + 256;
+  static_assert(TN * W * 128 * 4 <= STAGES * STAGE_BYTES, "the partial tile takes the ring's place");
+  static_assert(TMEM <= 256 && 2 * (SMEM_BYTES + 1024) <= 233472, "two CTAs per SM");
+};
+
+struct Skinny8Params {
+  int M, N, K;      // SWIGLU: N = F
+  int k_blocks, num_m_tiles;
+  const float* sa;  // [k_blocks, M]
+  const float* sb;  // [blocks of rows, k_blocks]
+  int split;        // SWIGLU: row offset of the up half
+  int c_fp32, add;
+  void* out;        // C, or Y
+  uint8_t* out2;    // AB, or null
+  float *sy, *sab;
+  uint32_t idesc;
+  uint32_t* status;
+  unsigned long long wait_limit_ns;
+  uint32_t kernel_id;
+};
+
+__device__ __forceinline__ void umma_f8_stage(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .b64 a, b;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, 0;\n\t"
+      "add.u64 a, %1, 2;\n\tadd.u64 b, %2, 2;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, 1;\n\t"
+      "add.u64 a, %1, 4;\n\tadd.u64 b, %2, 4;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, 1;\n\t"
+      "add.u64 a, %1, 6;\n\tadd.u64 b, %2, 6;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, 1;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc)
+      : "memory");
+}
+
+// 16 accumulator columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+// Sum of the cluster's copies of one partial, in rank order; the loads are in flight together.
+__device__ __forceinline__ float f8_cluster_sum(uint32_t addr, int splits) {
+  float v[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) v[r] = r < splits ? ld_cluster_f32(mapa_shared(addr, (uint32_t)r)) : 0.f;
+  float s = v[0];
+#pragma unroll
+  for (int r = 1; r < 8; ++r) s += v[r];
+  return s;
+}
+
+// Largest magnitude over the warp (NaNs left out).
+__device__ __forceinline__ float warp_max_abs(float v) {
+  v = fmaxf(fabsf(v), 0.f);
+  uint32_t r;
+  asm("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(__float_as_uint(v)));  // ordered as the floats are
+  return __uint_as_float(r);
+}
+
+template <int TN, bool SWIGLU>
+__global__ void __launch_bounds__(F8S_THREADS, TN * (SWIGLU ? 2 : 1) <= 64 ? 2 : 1)  // TN accumulators a thread
+    gemm_fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                           const Skinny8Params p) {
+  using C = F8SkinnyCfg<TN, SWIGLU>;
+  constexpr int S = C::STAGES, W = C::W;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* sScale = reinterpret_cast<float*>(smem + S * C::STAGE_BYTES);
+  float* sMax = sScale + C::SCALE_BYTES / 4;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sMax + C::MAX_BYTES / 4);
+  uint64_t* empty = full + S;
+  uint64_t* tfull = empty + S;
+  uint64_t* tempty = tfull + C::BUFS;
+  uint64_t* mma_done = tempty + C::BUFS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  DrainCtl* drain_ctl =
+      reinterpret_cast<DrainCtl*>((reinterpret_cast<uintptr_t>(tmem_slot + 1) + 15) & ~static_cast<uintptr_t>(15));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(&drain_ctl->abort);
+
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0);
+  const int lane = threadIdx.x % 32;
+  const int rank = (int)cluster_ctarank();
+  int splits;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(splits));
+  const int tile = (int)blockIdx.x / splits;
+  const int n_blk = tile / p.num_m_tiles;
+  const int m0 = (tile - n_blk * p.num_m_tiles) * TN;
+  const int kb0 = (int)((long long)rank * p.k_blocks / splits);
+  const int nkb = (int)((long long)(rank + 1) * p.k_blocks / splits) - kb0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < C::BUFS; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 4);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    drain_ctl->limit_ns = p.wait_limit_ns;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::TMEM);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+  const WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns, p.kernel_id};
+
+  float acc[W][TN];
+  if (warp == 0) {
+    if (lane == 0) {
+      // The weight is read once (evict-first); the rows of A by every tile.
+      const uint64_t hint_w = l2_policy_evict_first(), hint_x = l2_policy_evict_normal();
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0;
+      for (; issued < nkb; ++issued) {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, ctl, 0, kWaitEmpty)) break;
+        uint8_t* dst = smem + stage * C::STAGE_BYTES;
+        const int k0 = (kb0 + issued) * F8_BK;
+        mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
+        tma_load_2d(dst, &tmW, &full[stage], k0, n_blk * 128, hint_w);
+        if constexpr (SWIGLU) tma_load_2d(dst + F8_A_BYTES, &tmW, &full[stage], k0, p.split + n_blk * 128, hint_w);
+        tma_load_2d(dst + W * F8_A_BYTES, &tmX, &full[stage], k0, m0, hint_x);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      // Every copy has landed before this CTA's shared memory is used for anything else or released.
+      for (int i = issued > S ? issued - S : 0; i < issued; ++i)
+        mbar_wait(&full[i % S], (uint32_t)((i / S) & 1), ctl, 0, kWaitDrain);
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0;
+      const uint64_t desc0 = make_sdesc_sw128(smem_u32(smem), 16, 1024);
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!mbar_wait(&full[stage], phase, ctl, 1, kWaitFull)) break;
+        const int buf = kb % C::BUFS;
+        if (!mbar_wait(&tempty[buf], ((uint32_t)(kb / C::BUFS) & 1u) ^ 1u, ctl, 1, kWaitAccEmpty)) break;
+        tc_fence_after();
+        const uint64_t wd = desc0 + (uint64_t)((stage * C::STAGE_BYTES) >> 4);
+        const uint64_t xd = wd + ((W * F8_A_BYTES) >> 4);
+        const uint32_t d = tmem_base + (uint32_t)(buf * W * TN);
+        umma_f8_stage(d, wd, xd, p.idesc);
+        if constexpr (SWIGLU) umma_f8_stage(d + TN, wd + (F8_A_BYTES >> 4), xd, p.idesc);
+        umma_commit(&tfull[buf]);
+        umma_commit(&empty[stage]);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      umma_commit(mma_done);
+      mbar_wait(mma_done, 0, ctl, 1, kWaitDrain);
+    }
+  } else {
+    const int q = warp & 3;
+    const int t128 = q * 32 + lane;  // this thread's weight row
+    const uint32_t wctl = smem_u32(drain_ctl);
+    const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16);
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+      for (int t = 0; t < TN; ++t) acc[w][t] = 0.f;
+    // Scales of CHUNK / TN blocks at a time, A's times the weight's, fetched one chunk ahead.
+    constexpr int PER = C::CHUNK / 128;
+    constexpr int CH = C::CHUNK / TN;  // blocks per chunk
+    const float* sb = p.sb + (size_t)n_blk * p.k_blocks + kb0;
+    const float* sb2 = sb + (SWIGLU ? (size_t)(p.split / 128) * p.k_blocks : 0);
+    float pre[W][PER];
+    auto fetch = [&](int c0) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int idx = i * 128 + t128, kb = c0 + idx / TN, m = m0 + idx % TN;
+        const bool v = kb < nkb && m < p.M;
+        const float a = v ? __ldg(p.sa + (size_t)(kb0 + kb) * p.M + m) : 0.f;
+        pre[0][i] = v ? a * __ldg(sb + kb) : 0.f;
+        if constexpr (SWIGLU) pre[1][i] = v ? a * __ldg(sb2 + kb) : 0.f;
+      }
+    };
+    fetch(0);
+    int buf = 0;
+    uint32_t phase = 0;
+    for (int c0 = 0, par = 0; c0 < nkb; c0 += CH, par ^= 1) {
+      float* sc = sScale + par * W * C::CHUNK;
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) sc[w * C::CHUNK + i * 128 + t128] = pre[w][i];
+      asm volatile("bar.sync 1, 128;" ::: "memory");  // no drain warp leaves this loop early
+      if (c0 + CH < nkb) fetch(c0 + CH);
+      const int n = min(CH, nkb - c0);
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        mbar_wait_drain(smem_u32(&tfull[buf]), phase, wctl, (2 + q) << 8 | kWaitAccFull);
+        tc_fence_after();
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const float* s = sc + w * C::CHUNK + j * TN;
+#pragma unroll
+          for (int c = 0; c < TN; c += 16) {
+            float v[16];
+            tmem_ld16(taddr + (uint32_t)((buf * W + w) * TN + c), v);
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(s + c + i);
+              acc[w][c + i] = fmaf(v[i], f.x, acc[w][c + i]);
+              acc[w][c + i + 1] = fmaf(v[i + 1], f.y, acc[w][c + i + 1]);
+              acc[w][c + i + 2] = fmaf(v[i + 2], f.z, acc[w][c + i + 2]);
+              acc[w][c + i + 3] = fmaf(v[i + 3], f.w, acc[w][c + i + 3]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        mbar_arrive_if(smem_u32(&tempty[buf]), lane == 0);
+        if (++buf == C::BUFS) {
+          buf = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();  // the ring is free: every copy has landed and every MMA has read it
+  tc_fence_after();
+
+  // The partial tiles, [W][TN][128], in the ring's place.  Everything from here
+  // on is rolled loops over shared memory: it runs once per CTA, where unrolled
+  // code costs more to fetch than to run (M = 512, N = K = 4096: 108 us with
+  // this unrolled).
+  const int row = (warp & 3) * 32 + lane;
+  const bool drains = warp >= 2;
+  float* part = reinterpret_cast<float*>(smem);
+  if (drains) {
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+      for (int t = 0; t < TN; ++t) part[(w * TN + t) * 128 + row] = acc[w][t];
+  }
+  if (splits > 1) cluster_sync();
+  // This CTA's share of the tile's rows of A: [t0, t0 + share).
+  const int share = TN / splits, t0 = rank * share;
+  const int used = min(share, p.M - m0 - t0);  // rows that exist
+  const bool bad = *abort_flag != 0;
+  const int col = n_blk * 128 + row;
+  if (drains && !bad) {
+#pragma unroll 1
+    for (int t = 0; t < used; ++t) {
+      const int m = m0 + t0 + t;
+      float sum[W];
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float* own = part + (w * TN + t0 + t) * 128 + row;
+        sum[w] = splits == 1 ? *own : f8_cluster_sum(smem_u32(own), splits);
+      }
+      if constexpr (!SWIGLU) {
+        if (col < p.N) {
+          const size_t o = (size_t)m * p.N + col;
+          if (!p.c_fp32) {
+            static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(sum[0]);
+          } else {
+            float* c = static_cast<float*>(p.out) + o;
+            *c = p.add ? *c + sum[0] : sum[0];
+          }
+        }
+      } else {
+        // Only this CTA reads its own share of its own partial tile.
+        const float a = sum[0], b = sum[1], y = a * sigmoid_f(a) * b;
+        part[(t0 + t) * 128 + row] = a;
+        part[(TN + t0 + t) * 128 + row] = b;
+        const float my = warp_max_abs(y), ma = warp_max_abs(a), mb = warp_max_abs(b);
+        if (lane == 0) {
+          sMax[(t * 3 + 0) * 4 + (warp & 3)] = my;
+          sMax[(t * 3 + 1) * 4 + (warp & 3)] = ma;
+          sMax[(t * 3 + 2) * 4 + (warp & 3)] = mb;
+        }
+      }
+    }
+  }
+  if constexpr (SWIGLU) {
+    __syncthreads();
+    if (drains && !bad) {
+#pragma unroll 1
+      for (int t = 0; t < used; ++t) {
+        const int m = m0 + t0 + t;
+        float mx[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const float4 f = *reinterpret_cast<const float4*>(sMax + (t * 3 + i) * 4);
+          mx[i] = fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w));
+        }
+        const float a = part[(t0 + t) * 128 + row], b = part[(TN + t0 + t) * 128 + row];
+        static_cast<uint8_t*>(p.out)[(size_t)m * p.N + col] =
+            (uint8_t)fp8_pack2<FP8_E4M3>(a * sigmoid_f(a) * b * fp8_factor<FP8_E4M3>(mx[0]), 0.f);
+        if (p.out2 != nullptr) {
+          uint8_t* ab = p.out2 + (size_t)m * 2 * p.N + col;
+          ab[0] = (uint8_t)fp8_pack2<FP8_E4M3>(a * fp8_factor<FP8_E4M3>(mx[1]), 0.f);
+          ab[p.N] = (uint8_t)fp8_pack2<FP8_E4M3>(b * fp8_factor<FP8_E4M3>(mx[2]), 0.f);
+        }
+        if (row == 0) {
+          p.sy[(size_t)n_blk * p.M + m] = fp8_scale<FP8_E4M3>(mx[0]);
+          if (p.out2 != nullptr) {
+            p.sab[(size_t)n_blk * p.M + m] = fp8_scale<FP8_E4M3>(mx[1]);
+            p.sab[(size_t)(n_blk + p.split / 128) * p.M + m] = fp8_scale<FP8_E4M3>(mx[2]);
+          }
+        }
+      }
+    }
+  }
+  if (splits > 1) cluster_sync();  // peers are done with this CTA's partial tile
+  if (threadIdx.x == 0 && *abort_flag > 1 && p.status != nullptr) {  // a drain warp's wait
+    atomicCAS(p.status, 0u, 7u /* CODA_ERR_DEVICE_TIMEOUT */);
+    atomicCAS(p.status + 1, 0u, (p.kernel_id << 16) | (uint32_t)*abort_flag);
+  }
+  if (warp == 1) tmem_dealloc(tmem_base, C::TMEM);
+}
+
 }  // namespace coda

@@ -142,6 +142,26 @@ def test_gemm_any_number_of_rows(cuda_lib, M):
     assert (buf[M:] == 7.0).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(2001, 2064, 400), (4000, 1296, 1040), (1500, 3344, 272)])
+def test_gemm_ragged_tiles_of_many_rows(cuda_lib, M, N, K):
+    """Weights in blocks with enough rows for 256 x 256 tiles, ragged in every direction."""
+    args, kw, ref, err = _gemm_case(cuda_lib, M, N, K, False, False, True, "e4m3", "e4m3", False, seed=M)
+    buf = torch.full((M + 300, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    cuda_lib.gemm_fp8(*args, **kw, out=buf[:M])
+    check_close(num(buf[:M]), ref, err + BF16 * (np.abs(ref) + err), f"M={M}")
+    assert (buf[M:] == 7.0).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 16, 16), (5, 4096, 4096), (16, 2048, 8192), (20, 1040, 11008), (48, 512, 65536),
+                                   (200, 4096, 1024), (7, 128, 128), (64, 8192, 272), (100, 144, 2000)])
+def test_gemm_few_rows(cuda_lib, M, N, K):
+    """One to a few hundred rows: the reduction split over clusters of 1 to 8, with and without a remainder."""
+    args, kw, ref, err = _gemm_case(cuda_lib, M, N, K, False, False, True, "e4m3", "e5m2", True, seed=K)
+    one = cuda_lib.gemm_fp8(*args, **kw)
+    check_close(num(one), ref, err, "few rows")
+    assert torch.equal(one, cuda_lib.gemm_fp8(*args, **kw))
+
+
 @pytest.mark.parametrize("K", [1, 2, 127, 128, 129, 1000])
 def test_gemm_any_reduction_for_weight_gradients(cuda_lib, K):
     args, kw, ref, err = _gemm_case(cuda_lib, 272, 400, K, True, True, False, "e5m2", "e4m3", True, seed=K)
@@ -259,7 +279,7 @@ def test_rmsnorm_empty(cuda_lib):
 
 # ------------------------------------------------------------------ gate/up + SwiGLU and its backward
 
-@pytest.mark.parametrize("M,K,F", [(1, 128, 128), (3, 272, 256), (16, 512, 384), (33, 400, 128), (64, 640, 1024),
+@pytest.mark.parametrize("M,K,F", [(1, 128, 128), (3, 272, 256), (16, 512, 384), (33, 400, 128), (64, 640, 1024), (2, 4096, 128), (17, 2048, 640), (40, 1296, 256),
                                    (65, 128, 256), (130, 1040, 384), (300, 512, 1280), (520, 256, 2560)])
 def test_gemm_swiglu(cuda_lib, M, K, F):
     qa, sa, a64 = _operand(cuda_lib, _randn(M, K, seed=M), "rows")
