@@ -80,6 +80,22 @@ __device__ __forceinline__ void stg_v2(void* p, const uint2& v) {
   asm volatile("st.global.v2.u32 [%0], {%1,%2};" ::"l"(p), "r"(v.x), "r"(v.y) : "memory");
 }
 
+__device__ __forceinline__ void sts8(float* p, const float* f) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+__device__ __forceinline__ void lds8(const float* p, float* f) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+// Makes the compiler forget what it knows of a word, so that values formed from
+// it again are formed again instead of being kept.
+__device__ __forceinline__ void forget(uint32_t& w) { asm volatile("" : "+r"(w)); }
+__device__ __forceinline__ void forget(uint4& q) { forget(q.x), forget(q.y), forget(q.z), forget(q.w); }
+__device__ __forceinline__ void forget(uint2& q) { forget(q.x), forget(q.y); }
+
 // Largest of the 16 lanes that hold one row's 128 columns.
 __device__ __forceinline__ float max16(float v) {
 #pragma unroll
@@ -108,8 +124,9 @@ struct QuantParams {
 };
 
 template <int FMT, bool ROWS, bool COLS, bool BLOCKS, bool VEC>
-__global__ void __launch_bounds__(kQuantThreads) quant_fp8_kernel(const QuantParams p) {
-  __shared__ float smax[kQuantThreads / 32][128];
+__global__ void __launch_bounds__(kQuantThreads, 4) quant_fp8_kernel(const QuantParams p) {
+  __shared__ __align__(16) float smax[kQuantThreads / 32][128];
+  __shared__ __align__(16) float sfac[128];
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -175,32 +192,30 @@ __global__ void __launch_bounds__(kQuantThreads) quant_fp8_kernel(const QuantPar
 #pragma unroll
       for (int w = 0; w < kQuantThreads / 32; ++w) m = fmaxf(m, smax[w][0]);
       if (threadIdx.x == 0) p.sc[(size_t)tr * p.tiles_c + tc] = fp8_scale<FMT>(m);
+      m = fp8_factor<FMT>(m);
 #pragma unroll
       for (int j = 0; j < 8; ++j) cmax[j] = m;
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) cmax[j] = fmaxf(cmax[j], __shfl_xor_sync(0xffffffffu, cmax[j], 16));
-      if (lane < 16) {
+      if (lane < 16) sts8(&smax[warp][lane * 8], cmax);
+      __syncthreads();
+      if (threadIdx.x < 128) {  // one column each: maximum, scale, factor
+        float m = smax[0][threadIdx.x];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) smax[warp][lane * 8 + j] = cmax[j];
+        for (int w = 1; w < kQuantThreads / 32; ++w) m = fmaxf(m, smax[w][threadIdx.x]);
+        sfac[threadIdx.x] = fp8_factor<FMT>(m);
+        const int c = tc * 128 + threadIdx.x;
+        if (c < p.C) p.sc[(size_t)tr * p.C + c] = fp8_scale<FMT>(m);
       }
       __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kQuantThreads / 32; ++w) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) cmax[j] = fmaxf(cmax[j], smax[w][(lane % 16) * 8 + j]);
-      }
-      if (warp == 0 && lane < 16 && cv) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p.sc[(size_t)tr * p.C + c0 + j] = fp8_scale<FMT>(cmax[j]);
-      }
+      lds8(&sfac[(lane % 16) * 8], cmax);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) cmax[j] = fp8_factor<FMT>(cmax[j]);
 #pragma unroll
     for (int i = 0; i < kQuantRows; ++i) {
       const int row = r0 + 16 * i;
       float f[8];
+      forget(x[i]);
       values(i, f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= cmax[j];
@@ -326,49 +341,65 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_fp8_bwd_kernel(const RmsBwdPa
   for (int k = 0; k < CH; ++k)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dg[k][i] = 0.f;
-  int parity = 0;
-  for (int row = blockIdx.x; row < p.M; row += gridDim.x, parity ^= 1) {
+  // The next row's loads are issued before this row's reduction, where registers allow.
+  constexpr bool AHEAD = CH <= 2;
+  uint4 nq[CH], hq[CH], eq[CH];
+  float r = 0.f;
+  auto load = [&](int row) {
     const size_t base = (size_t)row * p.d;
-    const float r = p.r[row];
-    uint4 nq[CH], hq[CH];
+    r = p.r[row];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int c = (k * THREADS + threadIdx.x) * 8;
-      nq[k] = c < p.d ? ldg_nc_v4(p.dn + base + c) : make_uint4(0u, 0u, 0u, 0u);
-      hq[k] = c < p.d ? ldg_nc_v4(p.h + base + c) : make_uint4(0u, 0u, 0u, 0u);
+      const bool v = c < p.d;
+      nq[k] = v ? ldg_nc_v4(p.dn + base + c) : make_uint4(0u, 0u, 0u, 0u);
+      hq[k] = v ? ldg_nc_v4(p.h + base + c) : make_uint4(0u, 0u, 0u, 0u);
+      eq[k] = v && p.dh_in != nullptr ? ldg_nc_v4(p.dh_in + base + c) : make_uint4(0u, 0u, 0u, 0u);
     }
+  };
+  int row = blockIdx.x, parity = 0;
+  if (AHEAD && row < p.M) load(row);
+  for (; row < p.M; parity ^= 1) {
     float s = 0.f;
+    if (!AHEAD) load(row);
+    uint4 n0[CH], h0[CH], e0[CH];
+    const float r0 = r;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      n0[k] = nq[k];
+      h0[k] = hq[k];
+      e0[k] = eq[k];
+    }
+    const size_t base = (size_t)row * p.d;
+    row += gridDim.x;
+    if (AHEAD && row < p.M) load(row);
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int c = (k * THREADS + threadIdx.x) * 8;
       float n[8], h[8], g[8];
-      unpack8(nq[k], n);
-      unpack8(hq[k], h);
+      unpack8(n0[k], n);
+      unpack8(h0[k], h);
       unpack8(c < p.d ? ldg_nc_v4_l1(p.g + c) : make_uint4(0u, 0u, 0u, 0u), g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float nh = n[i] * h[i];
         s = fmaf(nh, g[i], s);
-        dg[k][i] = fmaf(nh, r, dg[k][i]);
+        dg[k][i] = fmaf(nh, r0, dg[k][i]);
       }
     }
     // Two scratch rows in turn: a thread may still read one while another starts the next row.
-    const float coef = block_sum_all<THREADS>(s, scratch[parity]) * p.inv_d * r * r * r;
+    const float coef = block_sum_all<THREADS>(s, scratch[parity]) * p.inv_d * r0 * r0 * r0;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int c = (k * THREADS + threadIdx.x) * 8;
       if (c >= p.d) continue;
-      float n[8], h[8], g[8];
-      unpack8(nq[k], n);
-      unpack8(hq[k], h);
+      float n[8], h[8], g[8], e[8];
+      unpack8(n0[k], n);
+      unpack8(h0[k], h);
+      unpack8(e0[k], e);
       unpack8(ldg_nc_v4_l1(p.g + c), g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) n[i] = fmaf(n[i] * g[i], r, -coef * h[i]);
-      if (p.dh_in != nullptr) {
-        unpack8(ldg_nc_v4(p.dh_in + base + c), g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) n[i] += g[i];
-      }
+      for (int i = 0; i < 8; ++i) n[i] = fmaf(n[i] * g[i], r0, fmaf(-coef, h[i], e[i]));
       stg_v4(p.dh + base + c, pack8(n));
     }
   }
@@ -404,9 +435,9 @@ struct SwigluBwd8Params {
 };
 
 template <int FMT, bool COLS>
-__global__ void __launch_bounds__(kSwBwdThreads) swiglu_fp8_bwd_kernel(const SwigluBwd8Params p) {
-  __shared__ float smax[COLS ? kSwBwdThreads / 32 : 1][3][128];
-  __shared__ float sfac[3][128];
+__global__ void __launch_bounds__(kSwBwdThreads, 2) swiglu_fp8_bwd_kernel(const SwigluBwd8Params p) {
+  __shared__ __align__(16) float smax[COLS ? kSwBwdThreads / 32 : 1][3][128];
+  __shared__ __align__(16) float sfac[3][128];
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -482,12 +513,11 @@ __global__ void __launch_bounds__(kSwBwdThreads) swiglu_fp8_bwd_kernel(const Swi
   }
   if constexpr (COLS) {
 #pragma unroll
-    for (int t = 0; t < 3; ++t)
+    for (int t = 0; t < 3; ++t) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float v = fmaxf(cmax[t][j], __shfl_xor_sync(0xffffffffu, cmax[t][j], 16));
-        if (lane < 16) smax[warp][t][lane * 8 + j] = v;
-      }
+      for (int j = 0; j < 8; ++j) cmax[t][j] = fmaxf(cmax[t][j], __shfl_xor_sync(0xffffffffu, cmax[t][j], 16));
+      if (lane < 16) sts8(&smax[warp][t][lane * 8], cmax[t]);
+    }
     __syncthreads();
     if (threadIdx.x < 3 * 128) {
       const int t = threadIdx.x / 128, c = threadIdx.x % 128;
@@ -509,18 +539,25 @@ __global__ void __launch_bounds__(kSwBwdThreads) swiglu_fp8_bwd_kernel(const Swi
     const int row = r0 + STEP * i;
     if (row >= p.M) continue;
     float da[8], db[8], y[8];
+    forget(dyq[i]);
+    forget(aq[i]);
+    forget(bq[i]);
     grads(i, da, db, y);
     const size_t oa = (size_t)row * 2 * p.F + c0, ob = oa + p.F;
     stg_v2(p.da + oa, fp8_pack8<FMT>(da, fa[i]));
     stg_v2(p.da + ob, fp8_pack8<FMT>(db, fbv[i]));
     if constexpr (COLS) {
       const int c = (lane % 16) * 8;
+      float f[8];
+      lds8(&sfac[0][c], f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        da[j] *= sfac[0][c + j];
-        db[j] *= sfac[1][c + j];
-        y[j] *= sfac[2][c + j];
-      }
+      for (int j = 0; j < 8; ++j) da[j] *= f[j];
+      lds8(&sfac[1][c], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) db[j] *= f[j];
+      lds8(&sfac[2][c], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] *= f[j];
       stg_v2(p.dac + oa, fp8_pack8<FMT>(da, 1.f));
       stg_v2(p.dac + ob, fp8_pack8<FMT>(db, 1.f));
       stg_v2(p.yc + (size_t)row * p.F + c0, fp8_pack8<FP8_E4M3>(y, 1.f));
