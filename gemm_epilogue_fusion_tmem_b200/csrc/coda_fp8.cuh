@@ -76,6 +76,14 @@ __device__ __forceinline__ uint2 ldg_nc_v2(const void* p) {
   asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
   return v;
 }
+__device__ __forceinline__ uint32_t ldg_nc_u32(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void stg_u32(void* p, uint32_t v) {
+  asm volatile("st.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
 __device__ __forceinline__ void stg_v2(void* p, const uint2& v) {
   asm volatile("st.global.v2.u32 [%0], {%1,%2};" ::"l"(p), "r"(v.x), "r"(v.y) : "memory");
 }
@@ -88,6 +96,13 @@ __device__ __forceinline__ void lds8(const float* p, float* f) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
   f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+// Largest of the warp's values, which are not negative (and then ordered as their bits are).
+__device__ __forceinline__ float warp_max(float v) {
+  uint32_t r;
+  asm("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(__float_as_uint(v)));
+  return __uint_as_float(r);
 }
 
 // Makes the compiler forget what it knows of a word, so that values formed from
@@ -415,15 +430,18 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_fp8_bwd_kernel(const RmsBwdPa
 
 // ------------------------------------------------------------------ SwiGLU backward from the 8-bit checkpoint
 
-// With s = sigmoid(a): da = dY b s (1 + a (1 - s)), db = dY a s, y = a s b.
-// One CTA per 128 tokens x 128 columns: dY (bf16) and the saved a, b (e4m3 and
-// one scale per row and 128 columns) are read once and held packed in
-// registers; the gradients are formed twice, once for the row and column
-// maxima and once to be rounded, which costs less than keeping 96 floats per
-// thread.  Outputs: dA = [da | db] in row blocks (operand of dgrad) and, with
-// COLS, dA and y in column blocks (operands of the two weight gradients).
+// With s = sigmoid(a), u = a s: da = dY b (s + u (1 - s)), db = dY u, y = u b.
+// One CTA per 128 tokens x 128 columns.  A warp holds 8 whole rows, a lane 4
+// columns of each, packed as they were read (dY bf16; a, b e4m3 with one scale
+// per row and 128 columns), so row maxima are one warp reduction and column
+// maxima stay in the lane until the warps meet in shared memory.  The gradients
+// are formed twice, once for the maxima and once to be rounded: keeping them
+// would take 96 registers and half the warps.  Outputs: dA = [da | db] in row
+// blocks (operand of dgrad) and, with COLS, dA and y in column blocks (operands
+// of the two weight gradients).
 constexpr int kSwBwdThreads = 512;
-constexpr int kSwBwdRows = 128 * 16 / kSwBwdThreads;  // rows per thread
+constexpr int kSwBwdWarps = kSwBwdThreads / 32;
+constexpr int kSwBwdRows = 128 / kSwBwdWarps;  // rows per warp
 
 struct SwigluBwd8Params {
   const __nv_bfloat16* dy;
@@ -436,94 +454,88 @@ struct SwigluBwd8Params {
 
 template <int FMT, bool COLS>
 __global__ void __launch_bounds__(kSwBwdThreads, 2) swiglu_fp8_bwd_kernel(const SwigluBwd8Params p) {
-  __shared__ __align__(16) float smax[COLS ? kSwBwdThreads / 32 : 1][3][128];
+  __shared__ __align__(16) float smax[COLS ? kSwBwdWarps : 1][3][128];
   __shared__ __align__(16) float sfac[3][128];
+  __shared__ __align__(16) float srow[128][4];  // per row: scales of a and b, factors of da and db
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int fb = p.F / 128;
   const int tr = blockIdx.x / fb, tc = blockIdx.x - tr * fb;
-  const int c0 = tc * 128 + (lane % 16) * 8;
-  const int r0 = tr * 128 + warp * 2 + lane / 16;  // then + 2 * warps per step
-  constexpr int STEP = kSwBwdThreads / 16;
-  uint4 dyq[kSwBwdRows];
-  uint2 aq[kSwBwdRows], bq[kSwBwdRows];
-  float as[kSwBwdRows], bs[kSwBwdRows];
+  const int c0 = tc * 128 + lane * 4;
+  const int r0 = tr * 128 + warp * kSwBwdRows;
+  uint2 dyq[kSwBwdRows];
+  uint32_t aq[kSwBwdRows], bq[kSwBwdRows];
 #pragma unroll
   for (int i = 0; i < kSwBwdRows; ++i) {
-    const int row = r0 + STEP * i;
-    dyq[i] = make_uint4(0u, 0u, 0u, 0u);
-    aq[i] = bq[i] = make_uint2(0u, 0u);
-    as[i] = bs[i] = 0.f;
+    const int row = r0 + i;
+    dyq[i] = make_uint2(0u, 0u);
+    aq[i] = bq[i] = 0u;
     if (row < p.M) {
-      dyq[i] = ldg_nc_v4(p.dy + (size_t)row * p.F + c0);
-      aq[i] = ldg_nc_v2(p.ab + (size_t)row * 2 * p.F + c0);
-      bq[i] = ldg_nc_v2(p.ab + (size_t)row * 2 * p.F + p.F + c0);
-      as[i] = p.sab[(size_t)tc * p.M + row];
-      bs[i] = p.sab[(size_t)(fb + tc) * p.M + row];
+      dyq[i] = ldg_nc_v2(p.dy + (size_t)row * p.F + c0);
+      aq[i] = ldg_nc_u32(p.ab + (size_t)row * 2 * p.F + c0);
+      bq[i] = ldg_nc_u32(p.ab + (size_t)row * 2 * p.F + p.F + c0);
     }
   }
-  // da, db, y of row step i.
+  // Lanes 0-7 fetch the rows' scales of a, lanes 8-15 those of b.
+  const int sr = r0 + lane % kSwBwdRows, half = lane / kSwBwdRows;
+  if (half < 2) srow[warp * kSwBwdRows + lane % kSwBwdRows][half] = sr < p.M ? p.sab[(size_t)(half * fb + tc) * p.M + sr] : 0.f;
+  __syncwarp();
+  // da, db, y of the warp's row i.
   auto grads = [&](int i, float* da, float* db, float* y) {
-    float dy[8], a[8], b[8];
-    unpack8(dyq[i], dy);
-    e4m3_unpack4(aq[i].x, a);
-    e4m3_unpack4(aq[i].y, a + 4);
-    e4m3_unpack4(bq[i].x, b);
-    e4m3_unpack4(bq[i].y, b + 4);
+    const float2 sc = *reinterpret_cast<const float2*>(srow[warp * kSwBwdRows + i]);
+    float a[4], b[4];
+    const float dy[4] = {bf16lo(dyq[i].x), bf16hi(dyq[i].x), bf16lo(dyq[i].y), bf16hi(dyq[i].y)};
+    e4m3_unpack4(aq[i], a);
+    e4m3_unpack4(bq[i], b);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float av = a[j] * as[i], bv = b[j] * bs[i];
+    for (int j = 0; j < 4; ++j) {
+      const float av = a[j] * sc.x, bv = b[j] * sc.y;
       const float s = sigmoid_f(av);
-      const float as_ = av * s;
-      da[j] = dy[j] * bv * fmaf(as_, 1.f - s, s);
-      db[j] = dy[j] * as_;
-      y[j] = as_ * bv;
+      const float u = av * s;
+      da[j] = dy[j] * bv * fmaf(u, 1.f - s, s);
+      db[j] = dy[j] * u;
+      y[j] = u * bv;
     }
   };
-  float cmax[3][8], fa[kSwBwdRows], fbv[kSwBwdRows];
+  float cmax[3][4];
 #pragma unroll
   for (int t = 0; t < 3; ++t)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) cmax[t][j] = 0.f;
+    for (int j = 0; j < 4; ++j) cmax[t][j] = 0.f;
+  float mine = 0.f;  // lane i: row i's maximum of da, lane 8 + i: of db
 #pragma unroll
   for (int i = 0; i < kSwBwdRows; ++i) {
-    float da[8], db[8], y[8];
+    float da[4], db[4], y[4];
     grads(i, da, db, y);
-    float ma = 0.f, mb = 0.f;
+    if constexpr (COLS) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      ma = fmaxf(ma, fabsf(da[j]));
-      mb = fmaxf(mb, fabsf(db[j]));
-      if constexpr (COLS) {
+      for (int j = 0; j < 4; ++j) {
         cmax[0][j] = fmaxf(cmax[0][j], fabsf(da[j]));
         cmax[1][j] = fmaxf(cmax[1][j], fabsf(db[j]));
         cmax[2][j] = fmaxf(cmax[2][j], fabsf(y[j]));
       }
     }
-    ma = max16(ma);
-    mb = max16(mb);
-    const int row = r0 + STEP * i;
-    if (lane % 16 == 0 && row < p.M) {
-      p.sda[(size_t)tc * p.M + row] = fp8_scale<FMT>(ma);
-      p.sda[(size_t)(fb + tc) * p.M + row] = fp8_scale<FMT>(mb);
-    }
-    fa[i] = fp8_factor<FMT>(ma);
-    fbv[i] = fp8_factor<FMT>(mb);
+    const float ma = warp_max(fmaxf(fmaxf(fmaxf(fabsf(da[0]), fabsf(da[1])), fmaxf(fabsf(da[2]), fabsf(da[3]))), 0.f));
+    const float mb = warp_max(fmaxf(fmaxf(fmaxf(fabsf(db[0]), fabsf(db[1])), fmaxf(fabsf(db[2]), fabsf(db[3]))), 0.f));
+    if (lane == i) mine = ma;
+    if (lane == kSwBwdRows + i) mine = mb;
   }
+  if (half < 2) {
+    srow[warp * kSwBwdRows + lane % kSwBwdRows][2 + half] = fp8_factor<FMT>(mine);
+    if (sr < p.M) p.sda[(size_t)(half * fb + tc) * p.M + sr] = fp8_scale<FMT>(mine);
+  }
+  __syncwarp();
   if constexpr (COLS) {
 #pragma unroll
-    for (int t = 0; t < 3; ++t) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) cmax[t][j] = fmaxf(cmax[t][j], __shfl_xor_sync(0xffffffffu, cmax[t][j], 16));
-      if (lane < 16) sts8(&smax[warp][t][lane * 8], cmax[t]);
-    }
+    for (int t = 0; t < 3; ++t)
+      *reinterpret_cast<float4*>(&smax[warp][t][lane * 4]) = make_float4(cmax[t][0], cmax[t][1], cmax[t][2], cmax[t][3]);
     __syncthreads();
     if (threadIdx.x < 3 * 128) {
       const int t = threadIdx.x / 128, c = threadIdx.x % 128;
       float m = smax[0][t][c];
 #pragma unroll
-      for (int w = 1; w < kSwBwdThreads / 32; ++w) m = fmaxf(m, smax[w][t][c]);
+      for (int w = 1; w < kSwBwdWarps; ++w) m = fmaxf(m, smax[w][t][c]);
       if (t == 2) {
         sfac[t][c] = fp8_factor<FP8_E4M3>(m);
         p.syc[(size_t)tr * p.F + tc * 128 + c] = fp8_scale<FP8_E4M3>(m);
@@ -534,33 +546,28 @@ __global__ void __launch_bounds__(kSwBwdThreads, 2) swiglu_fp8_bwd_kernel(const 
     }
     __syncthreads();
   }
+  float4 f[3];
+  if constexpr (COLS) {
+#pragma unroll
+    for (int t = 0; t < 3; ++t) f[t] = *reinterpret_cast<const float4*>(&sfac[t][lane * 4]);
+  }
 #pragma unroll
   for (int i = 0; i < kSwBwdRows; ++i) {
-    const int row = r0 + STEP * i;
-    if (row >= p.M) continue;
-    float da[8], db[8], y[8];
+    const int row = r0 + i;
+    if (row >= p.M) break;
+    float da[4], db[4], y[4];
     forget(dyq[i]);
     forget(aq[i]);
     forget(bq[i]);
     grads(i, da, db, y);
+    const float2 fr = *reinterpret_cast<const float2*>(&srow[warp * kSwBwdRows + i][2]);
     const size_t oa = (size_t)row * 2 * p.F + c0, ob = oa + p.F;
-    stg_v2(p.da + oa, fp8_pack8<FMT>(da, fa[i]));
-    stg_v2(p.da + ob, fp8_pack8<FMT>(db, fbv[i]));
+    stg_u32(p.da + oa, fp8_pack4<FMT>(da[0] * fr.x, da[1] * fr.x, da[2] * fr.x, da[3] * fr.x));
+    stg_u32(p.da + ob, fp8_pack4<FMT>(db[0] * fr.y, db[1] * fr.y, db[2] * fr.y, db[3] * fr.y));
     if constexpr (COLS) {
-      const int c = (lane % 16) * 8;
-      float f[8];
-      lds8(&sfac[0][c], f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) da[j] *= f[j];
-      lds8(&sfac[1][c], f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) db[j] *= f[j];
-      lds8(&sfac[2][c], f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] *= f[j];
-      stg_v2(p.dac + oa, fp8_pack8<FMT>(da, 1.f));
-      stg_v2(p.dac + ob, fp8_pack8<FMT>(db, 1.f));
-      stg_v2(p.yc + (size_t)row * p.F + c0, fp8_pack8<FP8_E4M3>(y, 1.f));
+      stg_u32(p.dac + oa, fp8_pack4<FMT>(da[0] * f[0].x, da[1] * f[0].y, da[2] * f[0].z, da[3] * f[0].w));
+      stg_u32(p.dac + ob, fp8_pack4<FMT>(db[0] * f[1].x, db[1] * f[1].y, db[2] * f[1].z, db[3] * f[1].w));
+      stg_u32(p.yc + (size_t)row * p.F + c0, fp8_pack4<FP8_E4M3>(y[0] * f[2].x, y[1] * f[2].y, y[2] * f[2].z, y[3] * f[2].w));
     }
   }
 }

@@ -702,14 +702,6 @@ __device__ __forceinline__ float f8_cluster_sum(uint32_t addr, int splits) {
   return s;
 }
 
-// Largest magnitude over the warp (NaNs left out).
-__device__ __forceinline__ float warp_max_abs(float v) {
-  v = fmaxf(fabsf(v), 0.f);
-  uint32_t r;
-  asm("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(__float_as_uint(v)));  // ordered as the floats are
-  return __uint_as_float(r);
-}
-
 template <int TN, bool SWIGLU>
 __global__ void __launch_bounds__(F8S_THREADS, TN * (SWIGLU ? 2 : 1) <= 64 ? 2 : 1)  // TN accumulators a thread
     gemm_fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -935,7 +927,9 @@ __global__ void __launch_bounds__(F8S_THREADS, TN * (SWIGLU ? 2 : 1) <= 64 ? 2 :
         const float a = sum[0], b = sum[1], y = a * sigmoid_f(a) * b;
         part[(t0 + t) * 128 + row] = a;
         part[(TN + t0 + t) * 128 + row] = b;
-        const float my = warp_max_abs(y), ma = warp_max_abs(a), mb = warp_max_abs(b);
+        // fmaxf leaves NaNs out of the maxima.
+        const float my = warp_max(fmaxf(fabsf(y), 0.f)), ma = warp_max(fmaxf(fabsf(a), 0.f)),
+                    mb = warp_max(fmaxf(fabsf(b), 0.f));
         if (lane == 0) {
           sMax[(t * 3 + 0) * 4 + (warp & 3)] = my;
           sMax[(t * 3 + 1) * 4 + (warp & 3)] = ma;
