@@ -27,6 +27,10 @@ template <int FMT>
 __host__ __device__ constexpr float fp8_max() {
   return FMT == FP8_E4M3 ? 448.f : 57344.f;
 }
+template <int V>
+struct IntC {
+  static constexpr int value = V;
+};
 constexpr float kFp8Tiny = 7.888609052210118e-31f;  // 2^-100
 
 // Scale of a block and the factor its values are multiplied by.
@@ -57,18 +61,6 @@ template <int FMT>
 __device__ __forceinline__ uint2 fp8_pack8(const float* f, float factor) {
   return make_uint2(fp8_pack4<FMT>(f[0] * factor, f[1] * factor, f[2] * factor, f[3] * factor),
                     fp8_pack4<FMT>(f[4] * factor, f[5] * factor, f[6] * factor, f[7] * factor));
-}
-
-// Four e4m3 values of a word to floats (exact: e4m3 is a subset of fp16).
-__device__ __forceinline__ void e4m3_unpack4(uint32_t w, float* f) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w >> (16 * i))));
-    const float2 v = __half22float2(*reinterpret_cast<__half2*>(&h));
-    f[2 * i] = v.x;
-    f[2 * i + 1] = v.y;
-  }
 }
 
 __device__ __forceinline__ uint2 ldg_nc_v2(const void* p) {
@@ -103,6 +95,55 @@ __device__ __forceinline__ float warp_max(float v) {
   uint32_t r;
   asm("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(__float_as_uint(v)));
   return __uint_as_float(r);
+}
+
+// Largest of three, magnitudes of the last two.
+__device__ __forceinline__ float max3_abs(float m, float a, float b) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+
+// Two floats in one register pair: the packed operations issue once for both.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(F2 a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// The two e4m3 values in a word's low half (exact: e4m3 is a subset of fp16).
+__device__ __forceinline__ F2 e4m3_pair(uint32_t w) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
+  const float2 v = __half22float2(*reinterpret_cast<__half2*>(&h));
+  return f2(v.x, v.y);
+}
+
+// Sigmoids of a pair: 1 / (1 + 2^(-x log2 e)).
+__device__ __forceinline__ F2 sigmoid2(F2 x) {
+  float e0, e1, s0, s1;
+  split(x * f2(-1.4426950408889634f, -1.4426950408889634f), e0, e1);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(s0) : "f"(e0));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(e1));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(1.f + s0));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(1.f + s1));
+  return f2(e0, e1);
 }
 
 // Makes the compiler forget what it knows of a word, so that values formed from
@@ -432,8 +473,8 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_fp8_bwd_kernel(const RmsBwdPa
 
 // With s = sigmoid(a), u = a s: da = dY b (s + u (1 - s)), db = dY u, y = u b.
 // One CTA per 128 tokens x 128 columns.  A warp holds 8 whole rows, a lane 4
-// columns of each, packed as they were read (dY bf16; a, b e4m3 with one scale
-// per row and 128 columns), so row maxima are one warp reduction and column
+// columns of each (dY bf16; a, b e4m3 with one scale per row and 128 columns),
+// so row maxima are one warp reduction and column
 // maxima stay in the lane until the warps meet in shared memory.  The gradients
 // are formed twice, once for the maxima and once to be rounded: keeping them
 // would take 96 registers and half the warps.  Outputs: dA = [da | db] in row
@@ -453,7 +494,7 @@ struct SwigluBwd8Params {
 };
 
 template <int FMT, bool COLS>
-__global__ void __launch_bounds__(kSwBwdThreads, 2) swiglu_fp8_bwd_kernel(const SwigluBwd8Params p) {
+__global__ void __launch_bounds__(kSwBwdThreads, 1024 / kSwBwdThreads) swiglu_fp8_bwd_kernel(const SwigluBwd8Params p) {
   __shared__ __align__(16) float smax[COLS ? kSwBwdWarps : 1][3][128];
   __shared__ __align__(16) float sfac[3][128];
   __shared__ __align__(16) float srow[128][4];  // per row: scales of a and b, factors of da and db
@@ -462,8 +503,11 @@ __global__ void __launch_bounds__(kSwBwdThreads, 2) swiglu_fp8_bwd_kernel(const 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int fb = p.F / 128;
   const int tr = blockIdx.x / fb, tc = blockIdx.x - tr * fb;
-  const int c0 = tc * 128 + lane * 4;
   const int r0 = tr * 128 + warp * kSwBwdRows;
+  // The tile's origin in [M, F] (of 2-byte dY and 1-byte y) and in [M, 2F], and
+  // this lane's 32-bit offsets in it.
+  const size_t t1 = (size_t)tr * 128 * p.F + tc * 128, t2 = (size_t)tr * 256 * p.F + tc * 128;
+  const uint32_t o1 = (uint32_t)(warp * kSwBwdRows) * p.F + lane * 4, o2 = (uint32_t)(warp * kSwBwdRows) * 2 * p.F + lane * 4;
   uint2 dyq[kSwBwdRows];
   uint32_t aq[kSwBwdRows], bq[kSwBwdRows];
 #pragma unroll
@@ -472,52 +516,54 @@ __global__ void __launch_bounds__(kSwBwdThreads, 2) swiglu_fp8_bwd_kernel(const 
     dyq[i] = make_uint2(0u, 0u);
     aq[i] = bq[i] = 0u;
     if (row < p.M) {
-      dyq[i] = ldg_nc_v2(p.dy + (size_t)row * p.F + c0);
-      aq[i] = ldg_nc_u32(p.ab + (size_t)row * 2 * p.F + c0);
-      bq[i] = ldg_nc_u32(p.ab + (size_t)row * 2 * p.F + p.F + c0);
+      dyq[i] = ldg_nc_v2(p.dy + t1 + (o1 + (uint32_t)i * p.F));
+      aq[i] = ldg_nc_u32(p.ab + t2 + (o2 + (uint32_t)i * 2 * p.F));
+      bq[i] = ldg_nc_u32(p.ab + t2 + p.F + (o2 + (uint32_t)i * 2 * p.F));
     }
   }
   // Lanes 0-7 fetch the rows' scales of a, lanes 8-15 those of b.
   const int sr = r0 + lane % kSwBwdRows, half = lane / kSwBwdRows;
   if (half < 2) srow[warp * kSwBwdRows + lane % kSwBwdRows][half] = sr < p.M ? p.sab[(size_t)(half * fb + tc) * p.M + sr] : 0.f;
   __syncwarp();
-  // da, db, y of the warp's row i.
-  auto grads = [&](int i, float* da, float* db, float* y) {
+  // da, db, y of two columns (pair k) of the warp's row i.
+  auto grads = [&](int i, int k, F2& da, F2& db, F2& y) {
     const float2 sc = *reinterpret_cast<const float2*>(srow[warp * kSwBwdRows + i]);
-    float a[4], b[4];
-    const float dy[4] = {bf16lo(dyq[i].x), bf16hi(dyq[i].x), bf16lo(dyq[i].y), bf16hi(dyq[i].y)};
-    e4m3_unpack4(aq[i], a);
-    e4m3_unpack4(bq[i], b);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float av = a[j] * sc.x, bv = b[j] * sc.y;
-      const float s = sigmoid_f(av);
-      const float u = av * s;
-      da[j] = dy[j] * bv * fmaf(u, 1.f - s, s);
-      db[j] = dy[j] * u;
-      y[j] = u * bv;
-    }
+    const uint32_t w = k ? dyq[i].y : dyq[i].x;
+    const F2 dy = f2(bf16lo(w), bf16hi(w));
+    const F2 a = e4m3_pair(aq[i] >> (16 * k)) * f2(sc.x, sc.x), b = e4m3_pair(bq[i] >> (16 * k)) * f2(sc.y, sc.y);
+    const F2 sg = sigmoid2(a);
+    const F2 u = a * sg;
+    da = dy * b * fma2(u, fma2(sg, f2(-1.f, -1.f), f2(1.f, 1.f)), sg);
+    db = dy * u;
+    y = u * b;
   };
   float cmax[3][4];
 #pragma unroll
   for (int t = 0; t < 3; ++t)
 #pragma unroll
     for (int j = 0; j < 4; ++j) cmax[t][j] = 0.f;
-  float mine = 0.f;  // lane i: row i's maximum of da, lane 8 + i: of db
+  float mine = 0.f;  // lane i: row i's maximum of da, lane kSwBwdRows + i: of db
 #pragma unroll
   for (int i = 0; i < kSwBwdRows; ++i) {
-    float da[4], db[4], y[4];
-    grads(i, da, db, y);
-    if constexpr (COLS) {
+    float ma = 0.f, mb = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        cmax[0][j] = fmaxf(cmax[0][j], fabsf(da[j]));
-        cmax[1][j] = fmaxf(cmax[1][j], fabsf(db[j]));
-        cmax[2][j] = fmaxf(cmax[2][j], fabsf(y[j]));
+    for (int k = 0; k < 2; ++k) {
+      F2 g[3];
+      grads(i, k, g[0], g[1], g[2]);
+      float x0, x1;
+#pragma unroll
+      for (int t = 0; t < 3; ++t) {
+        split(g[t], x0, x1);
+        if (t == 0) ma = max3_abs(ma, x0, x1);
+        if (t == 1) mb = max3_abs(mb, x0, x1);
+        if constexpr (COLS) {
+          cmax[t][2 * k] = fmaxf(cmax[t][2 * k], fabsf(x0));
+          cmax[t][2 * k + 1] = fmaxf(cmax[t][2 * k + 1], fabsf(x1));
+        }
       }
     }
-    const float ma = warp_max(fmaxf(fmaxf(fmaxf(fabsf(da[0]), fabsf(da[1])), fmaxf(fabsf(da[2]), fabsf(da[3]))), 0.f));
-    const float mb = warp_max(fmaxf(fmaxf(fmaxf(fabsf(db[0]), fabsf(db[1])), fmaxf(fabsf(db[2]), fabsf(db[3]))), 0.f));
+    ma = warp_max(ma);
+    mb = warp_max(mb);
     if (lane == i) mine = ma;
     if (lane == kSwBwdRows + i) mine = mb;
   }
@@ -546,28 +592,41 @@ __global__ void __launch_bounds__(kSwBwdThreads, 2) swiglu_fp8_bwd_kernel(const 
     }
     __syncthreads();
   }
-  float4 f[3];
-  if constexpr (COLS) {
+  {
 #pragma unroll
-    for (int t = 0; t < 3; ++t) f[t] = *reinterpret_cast<const float4*>(&sfac[t][lane * 4]);
-  }
+    for (int i = 0; i < kSwBwdRows; ++i) {
+      const int row = r0 + i;
+      if (row >= p.M) break;
+      forget(dyq[i]);
+      forget(aq[i]);
+      forget(bq[i]);
+      const float2 fr = *reinterpret_cast<const float2*>(&srow[warp * kSwBwdRows + i][2]);
+      uint32_t q[5] = {0u, 0u, 0u, 0u, 0u};  // da and db by rows; da, db and y by columns
 #pragma unroll
-  for (int i = 0; i < kSwBwdRows; ++i) {
-    const int row = r0 + i;
-    if (row >= p.M) break;
-    float da[4], db[4], y[4];
-    forget(dyq[i]);
-    forget(aq[i]);
-    forget(bq[i]);
-    grads(i, da, db, y);
-    const float2 fr = *reinterpret_cast<const float2*>(&srow[warp * kSwBwdRows + i][2]);
-    const size_t oa = (size_t)row * 2 * p.F + c0, ob = oa + p.F;
-    stg_u32(p.da + oa, fp8_pack4<FMT>(da[0] * fr.x, da[1] * fr.x, da[2] * fr.x, da[3] * fr.x));
-    stg_u32(p.da + ob, fp8_pack4<FMT>(db[0] * fr.y, db[1] * fr.y, db[2] * fr.y, db[3] * fr.y));
-    if constexpr (COLS) {
-      stg_u32(p.dac + oa, fp8_pack4<FMT>(da[0] * f[0].x, da[1] * f[0].y, da[2] * f[0].z, da[3] * f[0].w));
-      stg_u32(p.dac + ob, fp8_pack4<FMT>(db[0] * f[1].x, db[1] * f[1].y, db[2] * f[1].z, db[3] * f[1].w));
-      stg_u32(p.yc + (size_t)row * p.F + c0, fp8_pack4<FP8_E4M3>(y[0] * f[2].x, y[1] * f[2].y, y[2] * f[2].z, y[3] * f[2].w));
+      for (int k = 0; k < 2; ++k) {
+        F2 da, db, y;
+        grads(i, k, da, db, y);
+        auto put = [&](uint32_t& w, F2 x, auto fmt) {
+          float lo, hi;
+          split(x, lo, hi);
+          w |= fp8_pack2<decltype(fmt)::value>(lo, hi) << (16 * k);
+        };
+        put(q[0], da * f2(fr.x, fr.x), IntC<FMT>());
+        put(q[1], db * f2(fr.y, fr.y), IntC<FMT>());
+        if constexpr (COLS) {
+          put(q[2], da * F2{*reinterpret_cast<const uint64_t*>(&sfac[0][lane * 4 + 2 * k])}, IntC<FMT>());
+          put(q[3], db * F2{*reinterpret_cast<const uint64_t*>(&sfac[1][lane * 4 + 2 * k])}, IntC<FMT>());
+          put(q[4], y * F2{*reinterpret_cast<const uint64_t*>(&sfac[2][lane * 4 + 2 * k])}, IntC<FP8_E4M3>());
+        }
+      }
+      const uint32_t o = o2 + (uint32_t)i * 2 * p.F;
+      stg_u32(p.da + t2 + o, q[0]);
+      stg_u32(p.da + t2 + p.F + o, q[1]);
+      if constexpr (COLS) {
+        stg_u32(p.dac + t2 + o, q[2]);
+        stg_u32(p.dac + t2 + p.F + o, q[3]);
+        stg_u32(p.yc + t1 + (o1 + (uint32_t)i * p.F), q[4]);
+      }
     }
   }
 }
