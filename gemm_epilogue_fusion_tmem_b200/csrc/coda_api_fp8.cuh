@@ -10,6 +10,7 @@ namespace coda {
 namespace {
 
 constexpr int kScaleBlock = 128;  // values per scale along a blocked axis
+constexpr int kMax8Cols = 1 << 22;  // columns of the light passes' matrices: 32-bit offsets in a 128-row tile
 
 // Encoded maps of the 8-bit operands, cached per host thread as make_tmap's are.
 struct Tmap8Slot {
@@ -198,14 +199,15 @@ coda_status rms8_fwd(const RmsParams& p, void* stream) {
 // Widest row the norms hold in registers.
 constexpr int kRms8MaxD = 1024 * 4 * 8;
 
-// CTAs of the norm's backward: each keeps its share of dg in registers and
-// writes one partial row, so a few per SM.
-constexpr int kRms8BwdCtas = 592;
-int rms8_bwd_ctas(int M) { return std::min(M, kRms8BwdCtas); }
+// Threads per row of the norm's backward (8 columns each up to d = 8192), and
+// its CTAs: a thousand threads per SM, each CTA keeping its share of dg in
+// registers and writing one partial row.
+int rms8_bwd_threads(int d) { return d <= 1024 ? 128 : d <= 2048 ? 256 : d <= 4096 ? 512 : 1024; }
+int rms8_bwd_ctas(int M, int d) { return std::min(M, 148 * (1024 / rms8_bwd_threads(d))); }
 
 template <int T, int CH>
 coda_status rms8_bwd(const RmsBwdParams& p, void* stream) {
-  return launch_pass(CODA_KERNEL_RMSNORM_FP8_BWD, rmsnorm_fp8_bwd_kernel<T, CH>, rms8_bwd_ctas(p.M), T, stream, p);
+  return launch_pass(CODA_KERNEL_RMSNORM_FP8_BWD, rmsnorm_fp8_bwd_kernel<T, CH>, rms8_bwd_ctas(p.M, p.d), T, stream, p);
 }
 
 }  // namespace
@@ -221,7 +223,7 @@ coda_status coda_quant_fp8(const void* X, const float* rowvec_or_null, const voi
   const bool rows = Qr_or_null != nullptr || Sr_or_null != nullptr;
   const bool cols = Qc_or_null != nullptr || Sc_or_null != nullptr;
   if (R < 0 || C < 1 || !known_format(format)) return CODA_ERR_INVALID_ARG;
-  if (C % 16 != 0 || !tiles_fit(cdiv(R, kScaleBlock), cdiv(C, kScaleBlock))) return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (C % 16 != 0 || C > kMax8Cols || !tiles_fit(cdiv(R, kScaleBlock), cdiv(C, kScaleBlock))) return CODA_ERR_UNSUPPORTED_SHAPE;
   if (R == 0) return CODA_OK;
   if (!X || (!rows && !cols)) return CODA_ERR_INVALID_ARG;
   if (rows && (!Qr_or_null || !Sr_or_null)) return CODA_ERR_INVALID_ARG;
@@ -250,7 +252,7 @@ coda_status coda_quant_fp8(const void* X, const float* rowvec_or_null, const voi
 
 coda_status coda_quant_fp8_blocks(const void* W, void* Q, float* S, int R, int C, int format, void* stream) {
   if (R < 0 || C < 1 || !known_format(format)) return CODA_ERR_INVALID_ARG;
-  if (C % 16 != 0 || !tiles_fit(cdiv(R, kScaleBlock), cdiv(C, kScaleBlock))) return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (C % 16 != 0 || C > kMax8Cols || !tiles_fit(cdiv(R, kScaleBlock), cdiv(C, kScaleBlock))) return CODA_ERR_UNSUPPORTED_SHAPE;
   if (R == 0) return CODA_OK;
   if (!W || !Q || !S) return CODA_ERR_INVALID_ARG;
   if (!aligned16(W) || !aligned16(Q) || !aligned16(S)) return CODA_ERR_MISALIGNED;
@@ -347,7 +349,7 @@ coda_status coda_gemm_swiglu_fp8(const void* A, const float* SA, const void* Wgu
                                  void* AB_or_null, float* SAB_or_null, int M, int K, int F, void* ws, size_t ws_bytes,
                                  void* stream) {
   if (M < 0 || K < 1 || F < 1) return CODA_ERR_INVALID_ARG;
-  if (K % 16 != 0 || F % kScaleBlock != 0 || F > 0x3FFFFFFF || !tiles_fit(cdiv(M, 256), F / kScaleBlock))
+  if (K % 16 != 0 || F % kScaleBlock != 0 || F > kMax8Cols || !tiles_fit(cdiv(M, 256), F / kScaleBlock))
     return CODA_ERR_UNSUPPORTED_SHAPE;
   if (M == 0) return CODA_OK;
   if (!A || !SA || !Wgu || !SW || !Y || !SY || !ws) return CODA_ERR_INVALID_ARG;
@@ -412,7 +414,7 @@ coda_status coda_swiglu_fp8_bwd(const void* dY, const void* AB, const float* SAB
                                 void* dAc_or_null, float* SdAc_or_null, void* Yc_or_null, float* SYc_or_null, int M,
                                 int F, int format, void* stream) {
   if (M < 0 || F < 1 || !known_format(format)) return CODA_ERR_INVALID_ARG;
-  if (F % kScaleBlock != 0 || F > 0x3FFFFFFF || !tiles_fit(cdiv(M, kScaleBlock), F / kScaleBlock))
+  if (F % kScaleBlock != 0 || F > kMax8Cols || !tiles_fit(cdiv(M, kScaleBlock), F / kScaleBlock))
     return CODA_ERR_UNSUPPORTED_SHAPE;
   if (M == 0) return CODA_OK;
   if (!dY || !AB || !SAB || !dA || !SdA) return CODA_ERR_INVALID_ARG;
@@ -482,7 +484,7 @@ coda_status coda_rmsnorm_fp8_fwd(const void* X, const void* R_or_null, const voi
 
 size_t coda_rmsnorm_fp8_bwd_workspace_bytes(int M, int d) {
   if (M < 1 || d < 1) return kStatusBytes;
-  return kStatusBytes + (size_t)rms8_bwd_ctas(M) * d * 4;
+  return kStatusBytes + (size_t)rms8_bwd_ctas(M, d) * d * 4;
 }
 
 coda_status coda_rmsnorm_fp8_bwd(const void* dN, const void* H, const float* r, const void* g,
@@ -509,17 +511,17 @@ coda_status coda_rmsnorm_fp8_bwd(const void* dN, const void* H, const float* r, 
   p.M = M;
   p.d = d;
   p.inv_d = 1.0f / (float)d;
-  const int chunks = d / 8;
   coda_status st;
-  if (chunks <= 128) st = rms8_bwd<128, 1>(p, stream);
-  else if (chunks <= 256) st = rms8_bwd<256, 1>(p, stream);
-  else if (chunks <= 512) st = rms8_bwd<256, 2>(p, stream);
-  else if (chunks <= 1024) st = rms8_bwd<512, 2>(p, stream);
-  else if (chunks <= 2048) st = rms8_bwd<512, 4>(p, stream);
+  if (d <= 1024) st = rms8_bwd<128, 1>(p, stream);
+  else if (d <= 2048) st = rms8_bwd<256, 1>(p, stream);
+  else if (d <= 4096) st = rms8_bwd<512, 1>(p, stream);
+  else if (d <= 8192) st = rms8_bwd<1024, 1>(p, stream);
+  else if (d <= 16384) st = rms8_bwd<1024, 2>(p, stream);
   else st = rms8_bwd<1024, 4>(p, stream);
   if (st != CODA_OK) return st;
-  return launch_status(launch_ex(col_reduce_kernel, dim3(cdiv(d, 32)), dim3(COLRED_THREADS), 0,
-                                 static_cast<cudaStream_t>(stream), 1, (const float*)p.part, rms8_bwd_ctas(M), d, dg));
+  return launch_status(launch_ex(rmsnorm_fp8_dg_kernel, dim3(cdiv(d, 32)), dim3(kRmsDgThreads), 0,
+                                 static_cast<cudaStream_t>(stream), 1, (const float*)p.part, rms8_bwd_ctas(M, d), d,
+                                 dg));
 }
 
 }  // extern "C"

@@ -190,11 +190,14 @@ __global__ void __launch_bounds__(kQuantThreads, 4) quant_fp8_kernel(const Quant
   const int c0 = tc * 128 + (lane % 16) * 8;
   const int r0 = tr * 128 + warp * 2 + lane / 16;  // then + 16 per step
   const bool cv = c0 < p.C;
+  // The tile's first row, and this thread's 32-bit offset from it.
+  const size_t t0 = (size_t)tr * 128 * p.C;
+  const uint32_t o0 = (uint32_t)(r0 - tr * 128) * p.C + c0;
   uint4 x[kQuantRows];
 #pragma unroll
   for (int i = 0; i < kQuantRows; ++i) {
     const int row = r0 + 16 * i;
-    x[i] = (cv && row < p.R) ? ldg_nc_v4(p.x + (size_t)row * p.C + c0) : make_uint4(0u, 0u, 0u, 0u);
+    x[i] = (cv && row < p.R) ? ldg_nc_v4(p.x + t0 + (o0 + (uint32_t)(16 * i) * p.C)) : make_uint4(0u, 0u, 0u, 0u);
   }
   float cvec[8], rvec[kQuantRows];
   if constexpr (VEC) {
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(kQuantThreads, 4) quant_fp8_kernel(const Quant
       rmax = max16(rmax);
       const int row = r0 + 16 * i;
       if (row < p.R) {
-        if (cv) stg_v2(p.qr + (size_t)row * p.C + c0, fp8_pack8<FMT>(f, fp8_factor<FMT>(rmax)));
+        if (cv) stg_v2(p.qr + t0 + (o0 + (uint32_t)(16 * i) * p.C), fp8_pack8<FMT>(f, fp8_factor<FMT>(rmax)));
         if (lane % 16 == 0) p.sr[(size_t)tc * p.R + row] = fp8_scale<FMT>(rmax);
       }
     }
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(kQuantThreads, 4) quant_fp8_kernel(const Quant
       values(i, f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= cmax[j];
-      if (cv && row < p.R) stg_v2(p.qc + (size_t)row * p.C + c0, fp8_pack8<FMT>(f, 1.f));
+      if (cv && row < p.R) stg_v2(p.qc + t0 + (o0 + (uint32_t)(16 * i) * p.C), fp8_pack8<FMT>(f, 1.f));
     }
   }
 }
@@ -385,7 +388,7 @@ struct RmsBwdParams {
 
 // u = dN g;  dH = r u - H r^3 mean_j(u_j H_j) (+ dH_in);  dg partials: each CTA
 // takes every gridDim.x-th row and keeps sum_i dN_i H_i r_i of its columns in
-// registers, so one pass reads everything once; col_reduce_kernel adds the
+// registers, so one pass reads everything once; rmsnorm_fp8_dg_kernel adds the
 // CTAs' partials in a fixed order.
 template <int THREADS, int CH>
 __global__ void __launch_bounds__(THREADS) rmsnorm_fp8_bwd_kernel(const RmsBwdParams p) {
@@ -398,7 +401,7 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_fp8_bwd_kernel(const RmsBwdPa
 #pragma unroll
     for (int i = 0; i < 8; ++i) dg[k][i] = 0.f;
   // The next row's loads are issued before this row's reduction, where registers allow.
-  constexpr bool AHEAD = CH <= 2;
+  constexpr bool AHEAD = CH == 1;
   uint4 nq[CH], hq[CH], eq[CH];
   float r = 0.f;
   auto load = [&](int row) {
@@ -466,6 +469,30 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_fp8_bwd_kernel(const RmsBwdPa
     float* o = p.part + (size_t)blockIdx.x * p.d + c;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = dg[k][i];
+  }
+}
+
+// dg_j = sum of the CTAs' partials, 32 columns to a block: warp w adds rows w,
+// w + 32, ..., all in flight together, and the 32 sums are added in warp order.
+constexpr int kRmsDgThreads = 1024;
+__global__ void __launch_bounds__(kRmsDgThreads)
+    rmsnorm_fp8_dg_kernel(const float* __restrict__ part, int rows, int d, float* __restrict__ dg) {
+  __shared__ float sums[32][33];
+  griddep_wait();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int j = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (j < d) {
+#pragma unroll 8
+    for (int t = warp; t < rows; t += 32) s += part[(size_t)t * d + j];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && j < d) {
+    float tot = 0.f;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) tot += sums[w][lane];
+    dg[j] = tot;
   }
 }
 

@@ -131,7 +131,7 @@ coda_status coda_selftest_wait_timeout(void* ws, uint64_t limit_ns, void* stream
 #define CODA_KERNEL_QUANT_FP8 34          /* bf16 -> 8 bits (coda_quant_fp8, coda_quant_fp8_blocks) */
 #define CODA_KERNEL_SWIGLU_FP8_BWD 35     /* SwiGLU backward from the 8-bit [a | b] */
 #define CODA_KERNEL_RMSNORM_FP8_FWD 36    /* residual + RMSNorm -> 8 bits */
-#define CODA_KERNEL_RMSNORM_FP8_BWD 37    /* its backward (dg's column reduce is CODA_KERNEL_COL_REDUCE) */
+#define CODA_KERNEL_RMSNORM_FP8_BWD 37    /* its backward (without the short reduce of dg) */
 coda_status coda_profile_arm(int kernel, void* ev_start, void* ev_stop);
 
 /* ---------------------------------------------------------------- building block */
@@ -374,8 +374,8 @@ coda_status coda_qkv_rope_bwd(const void* dQKV, const void* X, const void* Wqkv,
  * Row and column scales have the blocked axis first.  Nothing is transposed:
  * a weight gradient dY^T X takes dY and X as they are stored, in columns form.
  *
- * Quantised matrices are dense, their column count a multiple of 16; any number
- * of rows.  Outputs may not overlap inputs.  These calls allocate nothing and,
+ * Quantised matrices are dense, their column count a multiple of 16 (at most
+ * 2^22 in the passes other than coda_gemm_fp8); any number of rows.  Outputs may not overlap inputs.  These calls allocate nothing and,
  * but for the norm's backward, need no scratch; `ws` of the two products holds
  * only the status word. */
 #define CODA_FP8_E4M3 0

@@ -107,7 +107,7 @@ def test_light_pass_refusals():
     for bad in (dict(X=None), dict(Qr=None), dict(Sr=None), dict(Qc=None), dict(Sc=None), dict(R=-1), dict(C=0),
                 dict(f=2), dict(Qr=None, Sr=None, Qc=None, Sc=None)):
         assert quant(**bad) == 1, bad
-    assert quant(C=72) == 2 and quant(X=P(8)) == 3 and quant(cv=P(24)) == 3 and quant(R=0, X=None) == 0
+    assert quant(C=72) == 2 and quant(C=(1 << 22) + 16) == 2 and quant(X=P(8)) == 3 and quant(cv=P(24)) == 3 and quant(R=0, X=None) == 0
     blocks = lambda W=ONE, Q=ONE, S=ONE, R=8, C=64, f=0: lib.coda_quant_fp8_blocks._fn(W, Q, S, R, C, f, None)
     assert blocks(W=None) == 1 and blocks(S=None) == 1 and blocks(f=7) == 1 and blocks(C=8) == 2
     assert blocks(Q=P(4)) == 3 and blocks(R=0) == 0
