@@ -18,8 +18,8 @@
 // operand's pair order), which makes it one 128-wide scale block of a weight,
 // and in the gate/up product 64 gate columns beside the same 64 up columns.
 //
-// Roles (384 threads, one CTA per SM): warp 0 TMA producer; warp 1 TMEM owner
-// and MMA issuer (pair's leader); warp 2 copies the scales of the blocks ahead
+// Roles (384 threads, one CTA per SM): warp 0 TMA producer; warp 1 TMEM owner;
+// warps 1 and 3 MMA issuers of the two halves (pair's leader); warp 2 scales; warp 2 copies the scales of the blocks ahead
 // into a ring of their own (read by the drain directly, their latency was paid
 // once per 128 of k: 743 us against NEWTIME for the 7B down projection); warps 4-7 drain half 0, warps 8-11 half 1,
 // one output row and 128 columns (128 fp32 registers) per thread.  The first
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);  // the two MMA issuers
     }
     for (int a = 0; a < 4; ++a) {
       mbar_init(&tfull[a], 1);
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       mbar_init(&sfull[a], 32);
       mbar_init(&sempty[a], F8_EPI_WARPS);
     }
-    mbar_init(mma_done, 1);
+    mbar_init(mma_done, 2);
     *abort_flag = 0;
     drain_ctl->limit_ns = p.wait_limit_ns;
     fence_mbar_init();
@@ -377,41 +377,39 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
           }
         }
       }
-    } else if (warp == 1 && rank == 0 && elect_one()) {
-      // ---------------------------------------------------------------- MMA issuer (pair's leader)
-      int stage = 0;
-      uint32_t phase = 0;
-      uint32_t it = 0;  // 128-deep blocks issued: parity selects the TMEM buffers
+    } else if ((warp == 1 || warp == 3) && rank == 0 && elect_one()) {
+      // ---------------------------------------------------------------- MMA issuers (pair's leader)
+      // One thread per half: per 128 of k a thread has two waits, four MMAs and
+      // two commits to get through, each some tens of clocks on an SM whose
+      // issue slots the drain fills; one thread for both halves needed 810
+      // clocks for what the tensor core does in 512.
+      const uint32_t half = (uint32_t)warp / 2;
+      const uint32_t wctl = smem_u32(drain_ctl);
+      uint32_t full_s = smem_u32(full), phase = 0, stage = 0;
+      uint32_t it = 0;  // 128-deep blocks issued: parity selects the TMEM buffer
       const uint64_t a_desc0 = make_sdesc_sw128(smem_u32(sA), 16, 1024);
-      const uint64_t b_desc0 = B_MN ? make_sdesc_sw64(smem_u32(sB), 16, 512) : make_sdesc_sw128(smem_u32(sB), 16, 1024);
-      bool ok = true;
-      for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
-        for (int kb = 0; kb < p.k_blocks && ok; ++kb, ++it) {
-          if (!mbar_wait(&full[stage], phase, ctl, 1, kWaitFull)) {
-            ok = false;
-            break;
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int buf = (int)(it & 1) * 2 + h;
-            if (!mbar_wait(&tempty[buf], ((it >> 1) & 1u) ^ 1u, ctl, 1, kWaitAccEmpty)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            // K-major: 32 bytes inside the 128-byte swizzled row; MN-major: 32 k
-            // rows of 128 bytes (A) or 64 bytes (B, one 64-row half per CTA).
-            umma_f8_stage_pair<A_MN ? 256 : 2, B_MN ? 128 : 2>(
-                tmem_base + (uint32_t)(buf * 128), a_desc0 + (uint64_t)(stage * (F8_A_BYTES >> 4)),
-                b_desc0 + (uint64_t)(stage * (F8_B_BYTES >> 4) + h * (8192 >> 4)), p.idesc);
-            umma_commit_pair_both(&tfull[buf]);
-          }
-          umma_commit_pair_both(&empty[stage]);  // both CTAs' operand tiles have been read
+      const uint64_t b_desc0 = (B_MN ? make_sdesc_sw64(smem_u32(sB), 16, 512) : make_sdesc_sw128(smem_u32(sB), 16, 1024)) +
+                               half * (8192 >> 4);
+      for (int tile = first_tile; tile < num_tiles; tile += tile_step) {
+#pragma unroll 1
+        for (int kb = p.k_blocks; kb > 0; --kb, ++it) {
+          const uint32_t buf = (it & 1) * 2 + half;
+          mbar_wait_drain(full_s + stage * 8, phase, wctl, 1 << 8 | kWaitFull);
+          mbar_wait_drain(smem_u32(tempty) + buf * 8, ((it >> 1) & 1u) ^ 1u, wctl, 1 << 8 | kWaitAccEmpty);
+          tc_fence_after();
+          // K-major: 32 bytes inside the 128-byte swizzled row; MN-major: 32 k
+          // rows of 128 bytes (A) or 64 bytes (B, one 64-row half per CTA).
+          umma_f8_stage_pair<A_MN ? 256 : 2, B_MN ? 128 : 2>(
+              tmem_base + buf * 128, a_desc0 + (uint64_t)(stage * (F8_A_BYTES >> 4)),
+              b_desc0 + (uint64_t)(stage * (F8_B_BYTES >> 4)), p.idesc);
+          umma_commit_pair_both(&tfull[buf]);
+          umma_commit_pair_both(&empty[stage]);  // with the other half's: both CTAs' operand tiles have been read
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
           }
         }
+        if (*abort_flag) break;
       }
       umma_commit_pair(mapa_shared(smem_u32(mma_done), 0));
       mbar_wait(mma_done, 0, ctl, 1, kWaitDrain);
