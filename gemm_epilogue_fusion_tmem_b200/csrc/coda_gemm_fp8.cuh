@@ -202,20 +202,25 @@ __device__ __forceinline__ float lds_here(const float* p) {
   return v;
 }
 
+// Scales of one 128-deep block for a drain thread: its row's and those of its
+// columns 0-63 and 64-127.
+struct F8Scales {
+  float a, b_lo, b_hi;
+};
+
 // acc += a * TMEM columns times b_lo (columns 0-63) or b_hi (64-127); with VEC
 // the columns have scales of their own in cs[128] (shared memory).  32 columns
-// are in flight while the 32 before them are added; the buffer is handed back
-// (release) as soon as the last have arrived: the row scale a is read again
-// behind that, since the multiply-adds depend on it and are otherwise scheduled
-// before the arrival, which then comes a third of the pass late.  Plain
-// multiply-adds: the packed fma.f32x2 runs at the same rate, and the moves that
-// pair its operands cost more than the issue slots it saves.
+// are in flight while the 32 before them are added; release() hands the buffer
+// back as soon as the last have arrived and reads the next block's scales.  The
+// row scale is read again behind it, since the multiply-adds depend on it and
+// are otherwise scheduled before the arrival, which then comes a third of the
+// pass late.  Plain multiply-adds: the packed fma.f32x2 runs at the same rate,
+// and the moves that pair its operands cost more than the issue slots it saves.
 template <bool VEC, typename Release>
-__device__ __forceinline__ void f8_promote(uint32_t taddr, const float* a, float b_lo, float b_hi, const float* cs,
+__device__ __forceinline__ void f8_promote(uint32_t taddr, const F8Scales& sc, const float* a, const float* cs,
                                            float (&acc)[128], Release release) {
   float v[2][32];
-  const float a0 = *a;
-  float lo = a0 * b_lo, hi = a0 * b_hi;
+  float lo = sc.a * sc.b_lo, hi = sc.a * sc.b_hi;
   tmem_ld32_async(taddr, v[0]);
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -223,6 +228,7 @@ __device__ __forceinline__ void f8_promote(uint32_t taddr, const float* a, float
     if (c < 3) {
       tmem_ld32_async(taddr + (c + 1) * 32, v[(c + 1) & 1]);
     } else {
+      const float b_hi = sc.b_hi;
       release();
       hi = lds_here(a) * b_hi;
     }
@@ -493,18 +499,27 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         const float* sc = sScale + (groups & 1) * GROUP_FLOATS;
         const float* cs = sc + F8_GROUP * 128 + (VEC ? h * 128 : EPI == F8_EPI_SWIGLU ? 0 : h);
         sc += q * 32 + lane;
+        // Half h is one block of a weight; a gate/up half holds columns of a gate and of an up block.
+        auto scales = [&](int ahead) {
+          F8Scales f;
+          f.a = lds_here(sc + ahead * 128);
+          f.b_lo = VEC ? 1.f : lds_here(cs + ahead * 2);
+          f.b_hi = EPI == F8_EPI_SWIGLU ? lds_here(cs + ahead * 2 + 1) : f.b_lo;
+          return f;
+        };
+        F8Scales cur = scales(0);
 #pragma unroll 1
         for (int n = min(left, F8_GROUP); n > 0; --n, ++it) {
-          // Half h is one block of a weight; a gate/up half holds columns of a gate and of an up block.
-          const float b_lo = VEC ? 1.f : cs[0];
-          const float b_hi = EPI == F8_EPI_SWIGLU ? cs[1] : b_lo;
           mbar_wait_drain(tfull_h, (it >> 1) & 1u, wctl, (2 + q) << 8 | kWaitAccFull);
           tc_fence_after();
-          f8_promote<VEC>(taddr_h, sc, b_lo, b_hi, cs, acc, [&] {
+          F8Scales next;
+          f8_promote<VEC>(taddr_h, cur, sc, cs, acc, [&] {
             tc_fence_before();
             __syncwarp();
             mbar_arrive_leader_if(tempty_h, one);
+            next = scales(1);  // behind the group's last block: not used
           });
+          cur = next;
           tfull_h ^= 16;
           tempty_h ^= 16;
           taddr_h ^= 256;
