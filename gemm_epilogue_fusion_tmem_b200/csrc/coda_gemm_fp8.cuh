@@ -19,12 +19,10 @@
 // and in the gate/up product 64 gate columns beside the same 64 up columns.
 //
 // Roles (384 threads, one CTA per SM): warp 0 TMA producer; warp 1 TMEM owner;
-// warps 1 and 3 MMA issuers of the two halves (pair's leader); warp 2 scales; warp 2 copies the scales of the blocks ahead
-// into a ring of their own (read by the drain directly, their latency was paid
-// once per 128 of k: 743 us against NEWTIME for the 7B down projection); warps 4-7 drain half 0, warps 8-11 half 1,
-// one output row and 128 columns (128 fp32 registers) per thread.  The first
-// warpgroup hands registers to the other two: 128 x 40 + 256 x 232 is the
-// launch's 384 x 168.  Waits are bounded (mbar_wait); a role that gives up
+// warps 1 and 3 MMA issuers of the two halves (pair's leader); warp 2 copies the
+// scales of 8 blocks ahead; warps 4-7 drain half 0, warps 8-11 half 1, one output
+// row and 128 columns (128 fp32 registers) per thread.  The first warpgroup hands
+// registers to the other two.  Waits are bounded; a role that gives up
 // records it and the CTA drains and exits.
 #pragma once
 
@@ -117,23 +115,32 @@ __device__ __forceinline__ void umma_f8_stage_pair(uint32_t d_tmem, uint64_t a_d
       : "memory");
 }
 
-// 32 accumulator columns of this thread's TMEM lane; valid after tmem_wait_ld.
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float (&v)[32]) {
+// 32 or 16 accumulator columns of this thread's TMEM lane as pairs of floats.
+__device__ __forceinline__ void tmem_ld_pairs(uint32_t taddr, F2 (&v)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
-        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
-        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
-        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      "{\n\t.reg .b32 t<32>;\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15,"
+      "t16,t17,t18,t19,t20,t21,t22,t23,t24,t25,t26,t27,t28,t29,t30,t31}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t"
+      "mov.b64 %0, {t0, t1}; mov.b64 %1, {t2, t3}; mov.b64 %2, {t4, t5}; mov.b64 %3, {t6, t7};\n\t"
+      "mov.b64 %4, {t8, t9}; mov.b64 %5, {t10, t11}; mov.b64 %6, {t12, t13}; mov.b64 %7, {t14, t15};\n\t"
+      "mov.b64 %8, {t16, t17}; mov.b64 %9, {t18, t19}; mov.b64 %10, {t20, t21}; mov.b64 %11, {t22, t23};\n\t"
+      "mov.b64 %12, {t24, t25}; mov.b64 %13, {t26, t27}; mov.b64 %14, {t28, t29}; mov.b64 %15, {t30, t31};\n\t}\n"
+      : "=l"(v[0].v), "=l"(v[1].v), "=l"(v[2].v), "=l"(v[3].v), "=l"(v[4].v), "=l"(v[5].v), "=l"(v[6].v), "=l"(v[7].v),
+        "=l"(v[8].v), "=l"(v[9].v), "=l"(v[10].v), "=l"(v[11].v), "=l"(v[12].v), "=l"(v[13].v), "=l"(v[14].v), "=l"(v[15].v)
       : "r"(taddr)
       : "memory");
 }
-// Wait for every TMEM load of this thread; ties `v` to a point after the wait.
-__device__ __forceinline__ void tmem_wait_ld(float (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[i])::"memory");
+__device__ __forceinline__ void tmem_ld_pairs(uint32_t taddr, F2 (&v)[8]) {
+  asm volatile(
+      "{\n\t.reg .b32 t<16>;\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t"
+      "mov.b64 %0, {t0, t1}; mov.b64 %1, {t2, t3}; mov.b64 %2, {t4, t5}; mov.b64 %3, {t6, t7};\n\t"
+      "mov.b64 %4, {t8, t9}; mov.b64 %5, {t10, t11}; mov.b64 %6, {t12, t13}; mov.b64 %7, {t14, t15};\n\t}\n"
+      : "=l"(v[0].v), "=l"(v[1].v), "=l"(v[2].v), "=l"(v[3].v), "=l"(v[4].v), "=l"(v[5].v), "=l"(v[6].v), "=l"(v[7].v)
+      : "r"(taddr)
+      : "memory");
 }
 
 // Asynchronous 4- or 16-byte copy to shared memory; zeros, and no read of src, when !valid.
@@ -202,49 +209,48 @@ __device__ __forceinline__ float lds_here(const float* p) {
   return v;
 }
 
+__device__ __forceinline__ void lds_here(const float* p, F2& a, F2& b) {
+  asm volatile("ld.volatile.shared.v2.u64 {%0, %1}, [%2];" : "=l"(a.v), "=l"(b.v) : "r"(smem_u32(p)) : "memory");
+}
+
 // Scales of one 128-deep block for a drain thread: its row's and those of its
 // columns 0-63 and 64-127.
 struct F8Scales {
   float a, b_lo, b_hi;
 };
 
-// acc += a * TMEM columns times b_lo (columns 0-63) or b_hi (64-127); with VEC
-// the columns have scales of their own in cs[128] (shared memory).  32 columns
-// are in flight while the 32 before them are added; release() hands the buffer
-// back as soon as the last have arrived and reads the next block's scales.  The
-// row scale is read again behind it, since the multiply-adds depend on it and
-// are otherwise scheduled before the arrival, which then comes a third of the
-// pass late.  Plain multiply-adds: the packed fma.f32x2 runs at the same rate,
-// and the moves that pair its operands cost more than the issue slots it saves.
+// acc += a * TMEM columns times b_lo (columns 0-63) or b_hi (64-127), two columns
+// to an instruction; with VEC the columns have scales of their own in cs[128]
+// (shared memory).  release() hands the buffer back as soon as the last columns
+// have arrived, and reads the next block's scales; the row scale is read again
+// behind it, since the multiply-adds that depend on it are otherwise scheduled
+// before the arrival.
 template <bool VEC, typename Release>
 __device__ __forceinline__ void f8_promote(uint32_t taddr, const F8Scales& sc, const float* a, const float* cs,
-                                           float (&acc)[128], Release release) {
-  float v[2][32];
-  float lo = sc.a * sc.b_lo, hi = sc.a * sc.b_hi;
-  tmem_ld32_async(taddr, v[0]);
+                                           F2 (&acc)[64], Release release) {
+  constexpr int N = VEC ? 8 : 16;  // pairs at a time: fewer where the column scales need registers too
+  const float lo = sc.a * sc.b_lo;
+  float hi = sc.a * sc.b_hi;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    tmem_wait_ld(v[c & 1]);
-    if (c < 3) {
-      tmem_ld32_async(taddr + (c + 1) * 32, v[(c + 1) & 1]);
-    } else {
+  for (int c = 0; c < 64; c += N) {
+    F2 v[N];
+    tmem_ld_pairs(taddr + 2 * c, v);
+    if (c == 64 - N) {
       const float b_hi = sc.b_hi;
       release();
       hi = lds_here(a) * b_hi;
     }
-    const float s = c < 2 ? lo : hi;
+    const F2 s = c < 32 ? f2(lo, lo) : f2(hi, hi);
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      float* x = v[c & 1] + i;
+    for (int i = 0; i < N; i += 2) {
       if constexpr (VEC) {
-        const float4 f = *reinterpret_cast<const float4*>(cs + c * 32 + i);
-        x[0] *= f.x;
-        x[1] *= f.y;
-        x[2] *= f.z;
-        x[3] *= f.w;
+        F2 f0, f1;
+        lds_here(cs + 2 * (c + i), f0, f1);
+        v[i] = v[i] * f0;
+        v[i + 1] = v[i + 1] * f1;
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[c * 32 + i + j] = fmaf(x[j], s, acc[c * 32 + i + j]);
+      acc[c + i] = fma2(v[i], s, acc[c + i]);
+      acc[c + i + 1] = fma2(v[i + 1], s, acc[c + i + 1]);
     }
   }
 }
@@ -489,9 +495,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       const int row = row0 + lane;
       const bool rv = row < p.M;
       const int col0 = EPI == F8_EPI_SWIGLU ? n_blk * 128 + h * 64 : n_blk * 256 + h * 128;
-      float acc[128];
+      F2 sums[64];
 #pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      for (int i = 0; i < 64; ++i) sums[i] = F2{0};
 #pragma unroll 1
       for (int left = p.k_blocks; left > 0; left -= F8_GROUP, ++groups) {
         mbar_wait_drain(smem_u32(&sfull[groups & 1]), (groups >> 1) & 1u, wctl, (2 + q) << 8 | kWaitFull);
@@ -513,7 +519,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
           mbar_wait_drain(tfull_h, (it >> 1) & 1u, wctl, (2 + q) << 8 | kWaitAccFull);
           tc_fence_after();
           F8Scales next;
-          f8_promote<VEC>(taddr_h, cur, sc, cs, acc, [&] {
+          f8_promote<VEC>(taddr_h, cur, sc, cs, sums, [&] {
             tc_fence_before();
             __syncwarp();
             mbar_arrive_leader_if(tempty_h, one);
@@ -530,6 +536,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         mbar_arrive_if(smem_u32(&sempty[groups & 1]), one);
       }
       if (__any_sync(0xffffffffu, *abort_flag)) break;  // some block above may not have been complete
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) split(sums[i], acc[2 * i], acc[2 * i + 1]);
       if constexpr (EPI == F8_EPI_BF16) {
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + (size_t)row * p.N + col0;
 #pragma unroll
