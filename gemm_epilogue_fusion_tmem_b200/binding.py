@@ -726,27 +726,33 @@ def _call(name: str, dev, *args) -> None:
             _check(getattr(_lib, name)(*args, torch._C._cuda_getCurrentRawStream(dev.index)), name)
 
 
-_status_ws: dict = {}
+_status_ws: dict = {}   # by device index
+_graph_status: list = []  # words of calls captured before their device's first eager one
 
 
 def _status_workspace(dev) -> Workspace:
     """The device's status word for calls that need no other scratch.  It is
-    never replaced, so captured graphs may keep its address; a call that is
-    itself being captured before the first eager one gets a word of its own in
-    the graph."""
-    ws = _status_ws.get(dev)
+    never replaced, so captured graphs may keep its address.  A call that is
+    captured before the first eager one gets a word of its own, which lives as
+    long as the process: its graph may be replayed at any time."""
+    ws = _status_ws.get(dev.index)
     if ws is None:
         ws = Workspace(256, dev)
-        if not torch.cuda.is_current_stream_capturing():
+        if torch.cuda.is_current_stream_capturing():
+            _graph_status.append(ws)
+        else:
             torch.cuda.current_stream(dev).synchronize()  # zeroed for every stream from here on
-            _status_ws[dev] = ws
+            _status_ws[dev.index] = ws
     return ws
 
 
 def fp8_status(device=None) -> tuple[int, int]:
     """Synchronise the current stream and return (status, detail) of the 8-bit
-    products that were given no workspace on this device."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    products that were given no workspace on this device (but for those captured
+    into a graph before the first eager one)."""
+    dev = torch.device("cuda" if device is None else device)
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
     with torch.cuda.device(dev):
         return _status_workspace(dev).query()
 

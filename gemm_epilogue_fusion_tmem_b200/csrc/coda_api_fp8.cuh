@@ -12,63 +12,25 @@ namespace {
 constexpr int kScaleBlock = 128;  // values per scale along a blocked axis
 constexpr int kMax8Cols = 1 << 22;  // columns of the light passes' matrices: 32-bit offsets in a 128-row tile
 
-// Encoded maps of the 8-bit operands, cached per host thread as make_tmap's are.
-struct Tmap8Slot {
-  const void* base;
-  long long rows, cols;
-  int box_cols, box_rows, swizzle;
-  CUtensorMap map;
-  bool valid;
-};
-constexpr int kTmap8Slots = 128;
-thread_local Tmap8Slot t_tmap8_cache[kTmap8Slots];
-
 // 8-bit matrix [rows][cols], boxes of box_cols x box_rows; out-of-range elements load as zero.
 bool make_tmap8(CUtensorMap* m, const void* base, long long rows, long long cols, int box_cols, int box_rows,
                 CUtensorMapSwizzle swizzle) {
-  uint64_t h = reinterpret_cast<uintptr_t>(base) >> 4;
-  for (uint64_t v : {(uint64_t)rows, (uint64_t)cols, (uint64_t)box_cols * 1024 + (uint64_t)box_rows,
-                     (uint64_t)swizzle})
-    h = (h ^ v) * 0x9E3779B97F4A7C15ull;
-  Tmap8Slot& s = t_tmap8_cache[(h >> 32) % kTmap8Slots];
-  if (s.valid && s.base == base && s.rows == rows && s.cols == cols &&
-      s.box_cols == box_cols && s.box_rows == box_rows && s.swizzle == (int)swizzle) {
-    *m = s.map;
-    return true;
-  }
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)cols};
   cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
-  if (enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return false;
-  s.base = base;
-  s.rows = rows;
-  s.cols = cols;
-  s.box_cols = box_cols;
-  s.box_rows = box_rows;
-  s.swizzle = (int)swizzle;
-  s.map = *m;
-  s.valid = true;
-  return true;
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A operand [m, k]: one box of 128 k x 128 m.  B operand [n, k]: boxes of 64 n
-// (a CTA's share of one column half).
-bool operand8_map_a(CUtensorMap* m, const void* p, long long mn, long long k, bool mn_major) {
-  if (mn_major) return make_tmap8(m, p, k, mn, 128, F8_BK, CU_TENSOR_MAP_SWIZZLE_128B);
-  return make_tmap8(m, p, mn, k, F8_BK, 128, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-bool operand8_map_b(CUtensorMap* m, const void* p, long long mn, long long k, bool mn_major) {
-  if (mn_major) return make_tmap8(m, p, k, mn, 64, F8_BK, CU_TENSOR_MAP_SWIZZLE_64B);
-  return make_tmap8(m, p, mn, k, F8_BK, 64, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-bool operand8_map_k(CUtensorMap* m, const void* p, long long mn, long long k, int box_mn) {
-  return make_tmap8(m, p, mn, k, F8_BK, box_mn, CU_TENSOR_MAP_SWIZZLE_128B);
+// Operand with logical shape [mn, k], stored [mn][k] or (mn_major) [k][mn]: boxes
+// of 128 k x box_mn, box_mn 64 or 128 when mn_major (its swizzle is the box's width).
+bool operand8_map(CUtensorMap* m, const void* p, long long mn, long long k, bool mn_major, int box_mn) {
+  if (!mn_major) return make_tmap8(m, p, mn, k, F8_BK, box_mn, CU_TENSOR_MAP_SWIZZLE_128B);
+  return make_tmap8(m, p, k, mn, box_mn, F8_BK, box_mn == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Few rows of A: the weight becomes the MMA's 128-row operand, the rows its
@@ -137,7 +99,7 @@ coda_status launch_gemm8_majors(const CUtensorMap& ta, const CUtensorMap& tb, bo
 }
 
 // Tiles of the few-rows kernel: 128 weight rows (and their partners in the up
-// half) x TN rows of A, split over k by a cluster.
+// half) x up to TN rows of A, split over k by a cluster.
 template <int TN, bool SWIGLU>
 coda_status launch_skinny8(const CUtensorMap& tw, const CUtensorMap& tx, Skinny8Params p, cudaStream_t s) {
   using C = F8SkinnyCfg<TN, SWIGLU>;
@@ -151,8 +113,7 @@ coda_status launch_skinny8(const CUtensorMap& tw, const CUtensorMap& tx, Skinny8
       return CODA_ERR_CUDA;
     ready[dev].store(true);
   }
-  p.num_m_tiles = cdiv(p.M, TN);
-  const int tiles = cdiv(p.N, 128) * p.num_m_tiles;
+  const int tiles = cdiv(p.N, 128);
   int splits = 1;
   while (splits < 8 && tiles * splits * 2 <= 2 * g_dev[dev].num_sms && splits * 4 <= p.k_blocks) splits *= 2;
   p.idesc = (p.idesc & ~(0x3Fu << 17)) | ((uint32_t)(TN >> 3) << 17);
@@ -300,7 +261,7 @@ coda_status coda_gemm_fp8(const void* A, const float* SA, const void* B, const f
   CUtensorMap ta, tb;
   if (M <= 64 && !a_mn && !b_mn && b_blocks) {
     const int tn = skinny8_rows(M);
-    if (!operand8_map_k(&tb, B, N, K, 128) || !operand8_map_k(&ta, A, M, K, tn)) return CODA_ERR_CUDA;
+    if (!operand8_map(&tb, B, N, K, false, 128) || !operand8_map(&ta, A, M, K, false, tn)) return CODA_ERR_CUDA;
     Skinny8Params p;
     std::memset(&p, 0, sizeof(p));
     p.M = M;
@@ -318,7 +279,7 @@ coda_status coda_gemm_fp8(const void* A, const float* SA, const void* B, const f
     if (tn == 32) return launch_skinny8<32, false>(tb, ta, p, s);
     return launch_skinny8<64, false>(tb, ta, p, s);
   }
-  if (!operand8_map_a(&ta, A, M, K, a_mn) || !operand8_map_b(&tb, B, N, K, b_mn)) return CODA_ERR_CUDA;
+  if (!operand8_map(&ta, A, M, K, a_mn, 128) || !operand8_map(&tb, B, N, K, b_mn, 64)) return CODA_ERR_CUDA;
   Gemm8Params p;
   std::memset(&p, 0, sizeof(p));
   p.M = M;
@@ -364,7 +325,7 @@ coda_status coda_gemm_swiglu_fp8(const void* A, const float* SA, const void* Wgu
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (M <= 32) {
     const int tn = skinny8_rows(M);
-    if (!operand8_map_k(&tb, Wgu, 2LL * F, K, 128) || !operand8_map_k(&ta, A, M, K, tn)) return CODA_ERR_CUDA;
+    if (!operand8_map(&tb, Wgu, 2LL * F, K, false, 128) || !operand8_map(&ta, A, M, K, false, tn)) return CODA_ERR_CUDA;
     Skinny8Params p;
     std::memset(&p, 0, sizeof(p));
     p.M = M;
@@ -383,7 +344,7 @@ coda_status coda_gemm_swiglu_fp8(const void* A, const float* SA, const void* Wgu
     if (tn == 16) return launch_skinny8<16, true>(tb, ta, p, s);
     return launch_skinny8<32, true>(tb, ta, p, s);
   }
-  if (!operand8_map_a(&ta, A, M, K, false) || !operand8_map_b(&tb, Wgu, 2LL * F, K, false)) return CODA_ERR_CUDA;
+  if (!operand8_map(&ta, A, M, K, false, 128) || !operand8_map(&tb, Wgu, 2LL * F, K, false, 64)) return CODA_ERR_CUDA;
   Gemm8Params p;
   std::memset(&p, 0, sizeof(p));
   p.M = M;

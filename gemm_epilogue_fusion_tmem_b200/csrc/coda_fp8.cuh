@@ -291,7 +291,6 @@ template <int THREADS>
 __device__ __forceinline__ float block_sum_all(float v, float* scratch) {
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if constexpr (THREADS == 32) return v;
   if ((threadIdx.x & 31) == 0) scratch[threadIdx.x / 32] = v;
   __syncthreads();
   float t = (threadIdx.x & 31) < THREADS / 32 ? scratch[threadIdx.x & 31] : 0.f;

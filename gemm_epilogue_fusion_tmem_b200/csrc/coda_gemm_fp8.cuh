@@ -182,10 +182,16 @@ __device__ __forceinline__ void mbar_wait_drain(uint32_t bar, uint32_t parity, u
       "r"(parity), "r"(ctl), "r"(detail)
       : "memory");
 }
+// Wait for copies or MMAs of this CTA's own, whether or not a role has given up:
+// they must not be in flight when their shared memory or TMEM is released.
+__device__ __forceinline__ void mbar_wait_own(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < limit_ns) {
+  }
+}
 // Arrive where `pred` is set, without a branch.
 __device__ __forceinline__ void mbar_arrive_if(uint32_t bar, uint32_t pred) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(
-                   bar),
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
                "r"(pred)
                : "memory");
 }
@@ -424,7 +430,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         if (*abort_flag) break;
       }
       umma_commit_pair(mapa_shared(smem_u32(mma_done), 0));
-      mbar_wait(mma_done, 0, ctl, 1, kWaitDrain);
+      mbar_wait_own(mma_done, 0, ctl.limit_ns);
     } else if (warp == 2) {
       // ---------------------------------------------------------------- scales (both CTAs)
       int st = 0;
@@ -621,12 +627,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     // memory is released.  Every wait here is bounded too.
     if (warp == 0 && lane == 0 && rank == 0) {
       const int first = issued > S ? issued - S : 0;
-      for (int i = first; i < issued; ++i) {
-        const uint32_t par = (uint32_t)((i / S) & 1);
-        const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(&full[i % S], par) && global_timer_ns() - t0 < ctl.limit_ns) {
-        }
-      }
+      for (int i = first; i < issued; ++i) mbar_wait_own(&full[i % S], (uint32_t)((i / S) & 1), ctl.limit_ns);
     }
     __syncthreads();
   }
@@ -653,10 +654,10 @@ template <int TN, bool SWIGLU>
 struct F8SkinnyCfg {
   static constexpr int W = SWIGLU ? 2 : 1;  // products per tile: gate and up
   static constexpr int STAGE_BYTES = W * F8_A_BYTES + TN * F8_BK;
-  static constexpr int STAGES = SWIGLU ? (TN == 16 ? 3 : 2) : TN <= 32 ? 5 : TN == 64 ? 4 : 3;
+  static constexpr int STAGES = SWIGLU ? (TN == 16 ? 3 : 2) : TN <= 32 ? 5 : 4;
   static constexpr int CHUNK = 1024 / W;  // scales staged at a time, per product
-  static constexpr int BUFS = TN * W <= 64 ? 4 : 256 / (TN * W);  // TMEM buffers
-  static constexpr uint32_t TMEM = BUFS * TN * W < 32 ? 32 : BUFS * TN * W;
+  static constexpr int BUFS = 4;  // TMEM buffers
+  static constexpr uint32_t TMEM = BUFS * TN * W;
   static constexpr int SCALE_BYTES = 2 * W * CHUNK * 4;
   // Row maxima of the 8-bit outputs: [TN][3][4 warps].
   static constexpr int MAX_BYTES = SWIGLU ? TN * 12 * 4 : 0;
@@ -666,8 +667,8 @@ struct F8SkinnyCfg {
 };
 
 struct Skinny8Params {
-  int M, N, K;      // SWIGLU: N = F
-  int k_blocks, num_m_tiles;
+  int M, N, K;      // M <= TN; SWIGLU: N = F
+  int k_blocks;
   const float* sa;  // [k_blocks, M]
   const float* sb;  // [blocks of rows, k_blocks]
   int split;        // SWIGLU: row offset of the up half
@@ -725,7 +726,7 @@ __device__ __forceinline__ float f8_cluster_sum(uint32_t addr, int splits) {
 }
 
 template <int TN, bool SWIGLU>
-__global__ void __launch_bounds__(F8S_THREADS, TN * (SWIGLU ? 2 : 1) <= 64 ? 2 : 1)  // TN accumulators a thread
+__global__ void __launch_bounds__(F8S_THREADS, 2)
     gemm_fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                            const Skinny8Params p) {
   using C = F8SkinnyCfg<TN, SWIGLU>;
@@ -749,9 +750,7 @@ __global__ void __launch_bounds__(F8S_THREADS, TN * (SWIGLU ? 2 : 1) <= 64 ? 2 :
   const int rank = (int)cluster_ctarank();
   int splits;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(splits));
-  const int tile = (int)blockIdx.x / splits;
-  const int n_blk = tile / p.num_m_tiles;
-  const int m0 = (tile - n_blk * p.num_m_tiles) * TN;
+  const int n_blk = (int)blockIdx.x / splits;
   const int kb0 = (int)((long long)rank * p.k_blocks / splits);
   const int nkb = (int)((long long)(rank + 1) * p.k_blocks / splits) - kb0;
 
@@ -798,7 +797,7 @@ __global__ void __launch_bounds__(F8S_THREADS, TN * (SWIGLU ? 2 : 1) <= 64 ? 2 :
         mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
         tma_load_2d(dst, &tmW, &full[stage], k0, n_blk * 128, hint_w);
         if constexpr (SWIGLU) tma_load_2d(dst + F8_A_BYTES, &tmW, &full[stage], k0, p.split + n_blk * 128, hint_w);
-        tma_load_2d(dst + W * F8_A_BYTES, &tmX, &full[stage], k0, m0, hint_x);
+        tma_load_2d(dst + W * F8_A_BYTES, &tmX, &full[stage], k0, 0, hint_x);
         if (++stage == S) {
           stage = 0;
           phase ^= 1u;
@@ -806,7 +805,7 @@ __global__ void __launch_bounds__(F8S_THREADS, TN * (SWIGLU ? 2 : 1) <= 64 ? 2 :
       }
       // Every copy has landed before this CTA's shared memory is used for anything else or released.
       for (int i = issued > S ? issued - S : 0; i < issued; ++i)
-        mbar_wait(&full[i % S], (uint32_t)((i / S) & 1), ctl, 0, kWaitDrain);
+        mbar_wait_own(&full[i % S], (uint32_t)((i / S) & 1), ctl.limit_ns);
     }
   } else if (warp == 1) {
     if (elect_one()) {
@@ -831,7 +830,7 @@ __global__ void __launch_bounds__(F8S_THREADS, TN * (SWIGLU ? 2 : 1) <= 64 ? 2 :
         }
       }
       umma_commit(mma_done);
-      mbar_wait(mma_done, 0, ctl, 1, kWaitDrain);
+      mbar_wait_own(mma_done, 0, ctl.limit_ns);
     }
   } else {
     const int q = warp & 3;
@@ -851,7 +850,7 @@ __global__ void __launch_bounds__(F8S_THREADS, TN * (SWIGLU ? 2 : 1) <= 64 ? 2 :
     auto fetch = [&](int c0) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int idx = i * 128 + t128, kb = c0 + idx / TN, m = m0 + idx % TN;
+        const int idx = i * 128 + t128, kb = c0 + idx / TN, m = idx % TN;
         const bool v = kb < nkb && m < p.M;
         const float a = v ? __ldg(p.sa + (size_t)(kb0 + kb) * p.M + m) : 0.f;
         pre[0][i] = v ? a * __ldg(sb + kb) : 0.f;
@@ -907,8 +906,8 @@ __global__ void __launch_bounds__(F8S_THREADS, TN * (SWIGLU ? 2 : 1) <= 64 ? 2 :
 
   // The partial tiles, [W][TN][128], in the ring's place.  Everything from here
   // on is rolled loops over shared memory: it runs once per CTA, where unrolled
-  // code costs more to fetch than to run (M = 512, N = K = 4096: 108 us with
-  // this unrolled).
+  // code costs more to fetch than to run (some 100 us over a launch of several
+  // waves).
   const int row = (warp & 3) * 32 + lane;
   const bool drains = warp >= 2;
   float* part = reinterpret_cast<float*>(smem);
@@ -921,13 +920,13 @@ __global__ void __launch_bounds__(F8S_THREADS, TN * (SWIGLU ? 2 : 1) <= 64 ? 2 :
   if (splits > 1) cluster_sync();
   // This CTA's share of the tile's rows of A: [t0, t0 + share).
   const int share = TN / splits, t0 = rank * share;
-  const int used = min(share, p.M - m0 - t0);  // rows that exist
+  const int used = min(share, p.M - t0);  // rows that exist
   const bool bad = *abort_flag != 0;
   const int col = n_blk * 128 + row;
   if (drains && !bad) {
 #pragma unroll 1
     for (int t = 0; t < used; ++t) {
-      const int m = m0 + t0 + t;
+      const int m = t0 + t;
       float sum[W];
 #pragma unroll
       for (int w = 0; w < W; ++w) {
@@ -965,7 +964,7 @@ __global__ void __launch_bounds__(F8S_THREADS, TN * (SWIGLU ? 2 : 1) <= 64 ? 2 :
     if (drains && !bad) {
 #pragma unroll 1
       for (int t = 0; t < used; ++t) {
-        const int m = m0 + t0 + t;
+        const int m = t0 + t;
         float mx[3];
 #pragma unroll
         for (int i = 0; i < 3; ++i) {

@@ -469,3 +469,148 @@ def test_profile_hook_names_the_8_bit_kernels(cuda_lib):
     torch.cuda.synchronize()
     for k, (a, b) in ev.items():
         assert 0 < a.elapsed_time(b) < 50, k
+
+
+# ------------------------------------------------------------------ addresses, streams, large tensors
+
+def _shifted(t):
+    """A copy of t whose storage starts 16 bytes behind a 32-byte boundary."""
+    skip = 16 // t.element_size()
+    buf = torch.zeros(t.numel() + 2 * skip, dtype=torch.uint8 if t.element_size() == 1 else t.dtype, device="cuda")
+    v = buf[skip:skip + t.numel()].view(t.dtype).view(t.shape)
+    v.copy_(t)
+    assert v.data_ptr() % 32 == 16 and v.is_contiguous()
+    return v
+
+
+def _same(a, b):
+    return torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("M", [20, 300])
+def test_operands_and_outputs_at_16_byte_addresses(cuda_lib, M):
+    B = cuda_lib
+    N, K, F = 272, 400, 256
+    args, kw, _, _ = _gemm_case(B, M, N, K, False, False, True, "e4m3", "e4m3", True, seed=1)
+    moved = [_shifted(t) if isinstance(t, torch.Tensor) else t for t in args]
+    for dtype in (torch.float32, torch.bfloat16):
+        kw["out_dtype"] = dtype
+        want = B.gemm_fp8(*args, **kw)
+        out = _shifted(torch.zeros(M, N, dtype=dtype, device="cuda"))
+        assert _same(B.gemm_fp8(*moved, **kw, out=out), want), dtype
+    kw["out_dtype"] = torch.float32
+    start = _randn(M, N, seed=2).cuda()
+    sums = [B.gemm_fp8(*args, **kw, accumulate=True, out=c) for c in (start.clone(), _shifted(start))]
+    assert _same(*sums)
+    x = B.quant_fp8(_bf(M, K, seed=3).cuda())
+    w = B.quant_fp8_blocks(_bf(2 * F, K, seed=4).cuda())
+    o = B.gemm_swiglu_fp8(x["Qr"], x["Sr"], w["Q"], w["S"])
+    at = {k: _shifted(torch.zeros_like(v, dtype=torch.float32).to(v.dtype)) for k, v in o.items()}
+    B.gemm_swiglu_fp8(x["Qr"], x["Sr"], w["Q"], w["S"], out=at)
+    for k in o:
+        assert _same(at[k], o[k]), k
+    dy = _bf(M, F, seed=5).cuda()
+    g = B.swiglu_fp8_bwd(dy, o["AB"], o["SAB"])
+    at = B.swiglu_fp8_bwd(_shifted(dy), _shifted(o["AB"]), _shifted(o["SAB"]),
+                          out={k: _shifted(torch.zeros_like(v, dtype=torch.float32).to(v.dtype)) for k, v in g.items()})
+    for k in g:
+        assert _same(at[k], g[k]), k
+
+
+def test_products_on_two_streams_at_once(cuda_lib):
+    """Launches of the tile kernel, of the few-rows kernel and of the passes interleaved on two streams."""
+    B = cuda_lib
+    x, w = _bf(1030, 512, seed=1).cuda(), _bf(768, 512, seed=2).cuda()
+    qx, qw = B.quant_fp8(x, cols=True), B.quant_fp8_blocks(w)
+    few = {k: v[:7].contiguous() if k == "Qr" else v[:, :7].contiguous() for k, v in qx.items() if k in ("Qr", "Sr")}
+    calls = [lambda: B.gemm_fp8(qx["Qr"], qx["Sr"], qw["Q"], qw["S"], 1030, 768, 512),
+             lambda: B.gemm_fp8(few["Qr"], few["Sr"], qw["Q"], qw["S"], 7, 768, 512),
+             lambda: B.gemm_fp8(qx["Qc"], qx["Sc"], qx["Qc"], qx["Sc"], 512, 512, 1030, a_mn_major=True, b_mn_major=True,
+                                b_blocks=False, out_dtype=torch.float32),
+             lambda: B.gemm_swiglu_fp8(qx["Qr"], qx["Sr"], qw["Q"], qw["S"])["Y"],
+             lambda: B.quant_fp8(x, cols=True)["Qc"]]
+    want = [c() for c in calls]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for rep in range(10):
+        for i, c in enumerate(calls):
+            with torch.cuda.stream(streams[(rep + i) % 2]):
+                got.append((i, c()))
+    torch.cuda.synchronize()
+    for i, t in got:
+        assert _same(t, want[i]), i
+    assert B.fp8_status() == (0, 0)
+
+
+TAIL = 40  # rows checked at the end of a tensor of more than 2^32 elements
+
+
+def test_quant_and_gemm_behind_32_bit_offsets(cuda_lib):
+    B = cuda_lib
+    R, C = 131200, 32768
+    assert (R - TAIL) * C > 2 ** 32
+    x = torch.randn(R, C, dtype=torch.bfloat16, device="cuda")
+    o = B.quant_fp8(x, cols=True)
+    tail = num(x[-128:])
+    assert R % 128 == 0
+    check_quant(o["Qr"][-TAIL:], o["Sr"][:, -TAIL:], tail[-TAIL:], "rows", "e4m3", "rows")
+    check_quant(o["Qc"][-128:], o["Sc"][-1:], tail, "cols", "e4m3", "cols")
+    del x, o["Qc"]
+    # The long matrix as an operand, and (few columns in) as an output.
+    qw, sw, w = _operand(B, _randn(16, C, seed=1), "blocks")
+    c = B.gemm_fp8(o["Qr"], o["Sr"], qw, sw, R, 16, C, out_dtype=torch.float32)
+    a = O.dequant(num(o["Qr"][-TAIL:]), num(o["Sr"][:, -TAIL:]), "rows")
+    check_close(num(c[-TAIL:]), a @ w.T, gemm_error(a, w, C), "long operand")
+    del o, c
+    qx, sx, a = _operand(B, _randn(R, 16, seed=2), "rows")
+    qw, sw, w = _operand(B, _randn(C, 16, seed=3), "blocks")
+    c = B.gemm_fp8(qx, sx, qw, sw, R, C, 16)
+    ref, err = a[-TAIL:] @ w.T, gemm_error(a[-TAIL:], w, 16)
+    check_close(num(c[-TAIL:]), ref, err + BF16 * (np.abs(ref) + err), "long output")
+    assert B.fp8_status() == (0, 0)
+
+
+def test_rmsnorm_behind_32_bit_offsets(cuda_lib):
+    M, d = 131200, 32768
+    x = torch.randn(M, d, dtype=torch.bfloat16, device="cuda")
+    g = (1 + 0.1 * _randn(d, seed=1)).bfloat16()
+    o = cuda_lib.rmsnorm_fp8_fwd(x, g.cuda(), 1e-5)
+    h = num(x[-TAIL:])
+    r, n = O.rmsnorm(h, num(g), 1e-5)
+    rel = (42 / 2 + 4 + 4) * FP32
+    check_close(num(o["r"][-TAIL:]), r, r * rel, "r")
+    check_quant(o["Q"][-TAIL:], o["S"][:, -TAIL:], n, "rows", "e4m3", "n", np.abs(n) * (rel + 2 * FP32))
+    r32 = o["r"]
+    del o
+    b = cuda_lib.rmsnorm_fp8_bwd(x, x, r32, g.cuda())
+    rr = num(r32[-TAIL:])
+    dh, _ = O.rmsnorm_bwd(h, h, rr, num(g), None)
+    u, rr = h * num(g), rr[:, None]
+    coef = np.abs(h) * rr ** 3 * np.mean(np.abs(u * h), axis=1, keepdims=True)
+    err = 50 * FP32 * coef + 6 * FP32 * (np.abs(rr * u) + np.abs(dh))
+    check_close(num(b["dH"][-TAIL:]), dh, err + BF16 * (np.abs(dh) + err), "dH")
+
+
+def test_swiglu_behind_32_bit_offsets(cuda_lib):
+    B = cuda_lib
+    M, F = 65664, 32768  # [a | b] has 2 F columns
+    assert (M - TAIL) * 2 * F > 2 ** 32 and M % 128 == 0
+    qx, sx, x = _operand(B, _randn(M, 16, seed=2), "rows")
+    qw, sw, w = _operand(B, _randn(2 * F, 16, seed=3), "blocks")
+    o = B.gemm_swiglu_fp8(qx, sx, qw, sw)
+    ab, err = x[-128:] @ w.T, gemm_error(x[-128:], w, 16)
+    a, b, ea, eb = ab[:, :F], ab[:, F:], err[:, :F], err[:, F:]
+    check_quant(o["AB"][-128:], o["SAB"][:, -128:], ab, "rows", "e4m3", "[a | b]", err)
+    check_quant(o["Y"][-128:], o["SY"][:, -128:], O.swiglu(a, b), "rows", "e4m3", "Y", swiglu_error(a, b, ea, eb))
+    del o["Y"]
+    dy = torch.randn(M, F, dtype=torch.bfloat16, device="cuda")
+    g = B.swiglu_fp8_bwd(dy, o["AB"], o["SAB"])
+    saved = O.dequant(num(o["AB"][-128:]), num(o["SAB"][:, -128:]), "rows")
+    a, b, t = saved[:, :F], saved[:, F:], num(dy[-128:])
+    dab, e = np.concatenate(O.swiglu_bwd(t, a, b), 1), np.concatenate(swiglu_bwd_error(t, a, b), 1)
+    check_quant(g["dA"][-128:], g["SdA"][:, -128:], dab, "rows", "e4m3", "dA rows", e)
+    check_quant(g["dAc"][-128:], g["SdAc"][-1:], dab, "cols", "e4m3", "dA cols", e)
+    check_quant(g["Yc"][-128:], g["SYc"][-1:], O.swiglu(a, b), "cols", "e4m3", "Y cols",
+                swiglu_error(a, b, np.abs(a) * FP32, np.abs(b) * FP32))
+    assert B.fp8_status() == (0, 0)
