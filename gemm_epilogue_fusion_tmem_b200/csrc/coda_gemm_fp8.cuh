@@ -131,15 +131,24 @@ __device__ __forceinline__ void tmem_ld_pairs(uint32_t taddr, F2 (&v)[16]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld_pairs(uint32_t taddr, F2 (&v)[8]) {
+// 16 TMEM lanes x 32 columns: in groups of 8 columns, this thread's words are two
+// neighbouring columns (2 (lane % 4)) of lane / 4 and the same of lane / 4 + 8.
+// The words are there after tmem_ld_wait.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
-      "{\n\t.reg .b32 t<16>;\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15}, [%8];\n\t"
-      "tcgen05.wait::ld.sync.aligned;\n\t"
-      "mov.b64 %0, {t0, t1}; mov.b64 %1, {t2, t3}; mov.b64 %2, {t4, t5}; mov.b64 %3, {t6, t7};\n\t"
-      "mov.b64 %4, {t8, t9}; mov.b64 %5, {t10, t11}; mov.b64 %6, {t12, t13}; mov.b64 %7, {t14, t15};\n\t}\n"
-      : "=l"(v[0].v), "=l"(v[1].v), "=l"(v[2].v), "=l"(v[3].v), "=l"(v[4].v), "=l"(v[5].v), "=l"(v[6].v), "=l"(v[7].v)
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+        "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+      :
       : "memory");
 }
 
@@ -215,8 +224,8 @@ __device__ __forceinline__ float lds_here(const float* p) {
   return v;
 }
 
-__device__ __forceinline__ void lds_here(const float* p, F2& a, F2& b) {
-  asm volatile("ld.volatile.shared.v2.u64 {%0, %1}, [%2];" : "=l"(a.v), "=l"(b.v) : "r"(smem_u32(p)) : "memory");
+__device__ __forceinline__ void lds_here(const float* p, F2& a) {
+  asm volatile("ld.volatile.shared.u64 %0, [%1];" : "=l"(a.v) : "r"(smem_u32(p)) : "memory");
 }
 
 // Scales of one 128-deep block for a drain thread: its row's and those of its
@@ -226,38 +235,73 @@ struct F8Scales {
 };
 
 // acc += a * TMEM columns times b_lo (columns 0-63) or b_hi (64-127), two columns
-// to an instruction; with VEC the columns have scales of their own in cs[128]
-// (shared memory).  release() hands the buffer back as soon as the last columns
+// to an instruction.  release() hands the buffer back as soon as the last columns
 // have arrived, and reads the next block's scales; the row scale is read again
 // behind it, since the multiply-adds that depend on it are otherwise scheduled
 // before the arrival.
-template <bool VEC, typename Release>
-__device__ __forceinline__ void f8_promote(uint32_t taddr, const F8Scales& sc, const float* a, const float* cs,
-                                           F2 (&acc)[64], Release release) {
-  constexpr int N = VEC ? 8 : 16;  // pairs at a time: fewer where the column scales need registers too
+template <typename Release>
+__device__ __forceinline__ void f8_promote(uint32_t taddr, const F8Scales& sc, const float* a, F2 (&acc)[64],
+                                           Release release) {
   const float lo = sc.a * sc.b_lo;
   float hi = sc.a * sc.b_hi;
 #pragma unroll
-  for (int c = 0; c < 64; c += N) {
-    F2 v[N];
+  for (int c = 0; c < 64; c += 16) {
+    F2 v[16];
     tmem_ld_pairs(taddr + 2 * c, v);
-    if (c == 64 - N) {
+    if (c == 48) {
       const float b_hi = sc.b_hi;
       release();
       hi = lds_here(a) * b_hi;
     }
     const F2 s = c < 32 ? f2(lo, lo) : f2(hi, hi);
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      if constexpr (VEC) {
-        F2 f0, f1;
-        lds_here(cs + 2 * (c + i), f0, f1);
-        v[i] = v[i] * f0;
-        v[i + 1] = v[i + 1] * f1;
-      }
-      acc[c + i] = fma2(v[i], s, acc[c + i]);
-      acc[c + i + 1] = fma2(v[i + 1], s, acc[c + i + 1]);
+    for (int i = 0; i < 16; ++i) acc[c + i] = fma2(v[i], s, acc[c + i]);
+  }
+}
+
+// The same where every column has a scale of its own, cs[128] in shared memory.
+// A thread that holds one row would read all 128 of them: 512 bytes a thread, and
+// with 256 threads the reads alone take 1024 clocks per 128 of k.  So a thread
+// holds 4 rows (lane / 4 and 8, 16, 24 further, scales a[8 i]) and 32 columns
+// (2 (lane % 4) and the next in each group of 8), and reads a quarter of that
+// (4096 x 4096 x 8192: 193 -> 168 us).  The next columns' TMEM load and scales
+// are in flight while these are added.
+// acc[(half * 16 + group) * 2 + i]: rows 16 half + 8 i.
+template <typename Release>
+__device__ __forceinline__ void f8_promote_columns(uint32_t taddr, const float (&sc)[4], const float* a,
+                                                   const float* cs, F2 (&acc)[64], Release release) {
+  uint32_t t[2][16];
+  float r[4] = {sc[0], sc[1], sc[2], sc[3]};
+  F2 f[4], ahead[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) lds_here(cs + g * 8, ahead[g]);
+  tmem_ld_16x32(taddr, t[0]);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {  // 32 columns c / 2, 16 rows c % 2
+    const int h = c % 2;
+    if (h == 0) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) f[g] = ahead[g];
     }
+    tmem_ld_wait(t[h]);
+    if (c < 7) tmem_ld_16x32(taddr + (uint32_t)((c + 1) / 2 * 32) + ((uint32_t)((c + 1) % 2 * 16) << 16), t[h ^ 1]);
+    if (h == 0 && c < 6) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) lds_here(cs + (c + 2) * 16 + g * 8, ahead[g]);
+    }
+    if (c == 7) {
+      release();
+      r[2] = lds_here(a + 16);
+      r[3] = lds_here(a + 24);
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        F2& s = acc[(h * 16 + c / 2 * 4 + g) * 2 + i];
+        const F2 x = f2(__uint_as_float(t[h][g * 4 + 2 * i]), __uint_as_float(t[h][g * 4 + 2 * i + 1])) * f[g];
+        s = fma2(x, f2(r[h * 2 + i], r[h * 2 + i]), s);
+      }
   }
 }
 
@@ -271,6 +315,11 @@ __device__ __forceinline__ void f8_store32(void* dst, const uint32_t (&w)[8], bo
     stg_v4(dst, make_uint4(w[0], w[1], w[2], w[3]));
     stg_v4(static_cast<uint8_t*>(dst) + 16, make_uint4(w[4], w[5], w[6], w[7]));
   }
+}
+__device__ __forceinline__ void f8_add8(float* dst, F2 v) {
+  float lo, hi;
+  split(v, lo, hi);
+  asm volatile("red.global.add.v2.f32 [%0], {%1,%2};" ::"l"(dst), "f"(lo), "f"(hi) : "memory");
 }
 __device__ __forceinline__ void f8_add16(float* dst, const float* f) {
   asm volatile("red.global.add.v4.f32 [%0], {%1,%2,%3,%4};" ::"l"(dst), "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3])
@@ -509,29 +558,40 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         mbar_wait_drain(smem_u32(&sfull[groups & 1]), (groups >> 1) & 1u, wctl, (2 + q) << 8 | kWaitFull);
         if (*abort_flag) break;
         const float* sc = sScale + (groups & 1) * GROUP_FLOATS;
-        const float* cs = sc + F8_GROUP * 128 + (VEC ? h * 128 : EPI == F8_EPI_SWIGLU ? 0 : h);
-        sc += q * 32 + lane;
+        const float* cs = sc + F8_GROUP * 128 + (VEC ? h * 128 + lane % 4 * 2 : EPI == F8_EPI_SWIGLU ? 0 : h);
+        sc += q * 32 + (VEC ? lane / 4 : lane);
         // Half h is one block of a weight; a gate/up half holds columns of a gate and of an up block.
-        auto scales = [&](int ahead) {
-          F8Scales f;
-          f.a = lds_here(sc + ahead * 128);
-          f.b_lo = VEC ? 1.f : lds_here(cs + ahead * 2);
-          f.b_hi = EPI == F8_EPI_SWIGLU ? lds_here(cs + ahead * 2 + 1) : f.b_lo;
-          return f;
+        F8Scales cur, next;
+        float rows[4], next_rows[4];
+        auto scales = [&](int ahead, F8Scales& f, float (&r)[4]) {
+          if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = lds_here(sc + ahead * 128 + 8 * i);
+          } else {
+            f.a = lds_here(sc + ahead * 128);
+            f.b_lo = lds_here(cs + ahead * 2);
+            f.b_hi = EPI == F8_EPI_SWIGLU ? lds_here(cs + ahead * 2 + 1) : f.b_lo;
+          }
         };
-        F8Scales cur = scales(0);
+        scales(0, cur, rows);
 #pragma unroll 1
         for (int n = min(left, F8_GROUP); n > 0; --n, ++it) {
           mbar_wait_drain(tfull_h, (it >> 1) & 1u, wctl, (2 + q) << 8 | kWaitAccFull);
           tc_fence_after();
-          F8Scales next;
-          f8_promote<VEC>(taddr_h, cur, sc, cs, sums, [&] {
+          auto release = [&] {
             tc_fence_before();
             __syncwarp();
             mbar_arrive_leader_if(tempty_h, one);
-            next = scales(1);  // behind the group's last block: not used
-          });
-          cur = next;
+            scales(1, next, next_rows);  // behind the group's last block: not used
+          };
+          if constexpr (VEC) {
+            f8_promote_columns(taddr_h, rows, sc, cs, sums, release);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rows[i] = next_rows[i];
+          } else {
+            f8_promote(taddr_h, cur, sc, sums, release);
+            cur = next;
+          }
           tfull_h ^= 16;
           tempty_h ^= 16;
           taddr_h ^= 256;
@@ -542,74 +602,98 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         mbar_arrive_if(smem_u32(&sempty[groups & 1]), one);
       }
       if (__any_sync(0xffffffffu, *abort_flag)) break;  // some block above may not have been complete
-      float acc[128];
+      if constexpr (VEC) {
+        // Four lanes hold 8 neighbouring columns of a row.
 #pragma unroll
-      for (int i = 0; i < 64; ++i) split(sums[i], acc[2 * i], acc[2 * i + 1]);
-      if constexpr (EPI == F8_EPI_BF16) {
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + (size_t)row * p.N + col0;
+        for (int i = 0; i < 4; ++i) {
+          const int m = row0 + lane / 4 + 8 * i, c0 = col0 + lane % 4 * 2;
+          if (m >= p.M) break;
+          const size_t o = (size_t)m * p.N + c0;
 #pragma unroll
-        for (int c = 0; c < 128; c += 16) {
-          if (!rv || col0 + c >= p.N) break;
-          uint32_t w[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(acc[c + 2 * i], acc[c + 2 * i + 1]);
-          f8_store32(o + c, w, p.wide);
-        }
-      } else if constexpr (EPI == F8_EPI_F32) {
-        float* o = static_cast<float*>(p.out) + (size_t)row * p.N + col0;
-        if (p.add) {
-#pragma unroll
-          for (int c = 0; c < 128; c += 4) {
-            if (!rv || col0 + c >= p.N) break;
-            f8_add16(o + c, acc + c);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 128; c += 8) {
-            if (!rv || col0 + c >= p.N) break;
-            uint32_t w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(acc[c + i]);
-            f8_store32(o + c, w, p.wide);
+          for (int g = 0; g < 16; ++g) {
+            if (col0 + 8 * g >= p.N) break;
+            const F2 v = sums[(i / 2 * 16 + g) * 2 + i % 2];
+            float lo, hi;
+            split(v, lo, hi);
+            if constexpr (EPI == F8_EPI_BF16) {
+              stg_u32(static_cast<__nv_bfloat16*>(p.out) + o + 8 * g, pack_bf16x2(lo, hi));
+            } else if (p.add) {
+              f8_add8(static_cast<float*>(p.out) + o + 8 * g, v);
+            } else {
+              stg_v2(static_cast<float*>(p.out) + o + 8 * g, make_uint2(__float_as_uint(lo), __float_as_uint(hi)));
+            }
           }
         }
       } else {
-        // Columns 0-63 are a, 64-127 the same columns of b.  One scale per row
-        // and 128 columns: the two halves exchange their maxima.
-        float my = 0.f, ma = 0.f, mb = 0.f;
+        float acc[128];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          my = fmaxf(my, fabsf(acc[i] * sigmoid_f(acc[i]) * acc[64 + i]));
-          ma = fmaxf(ma, fabsf(acc[i]));
-          mb = fmaxf(mb, fabsf(acc[64 + i]));
-        }
-        float* x = sXch + (tiles_done & 1) * 768 + q * 32 + lane;
-        x[h * 384] = my;
-        x[h * 384 + 128] = ma;
-        x[h * 384 + 256] = mb;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(xch);
-        mbar_wait_drain(smem_u32(xch), tiles_done & 1u, wctl, (2 + q) << 8 | kWaitAccFull);
-        if (__any_sync(0xffffffffu, *abort_flag)) break;
-        my = fmaxf(my, x[(h ^ 1) * 384]);
-        ma = fmaxf(ma, x[(h ^ 1) * 384 + 128]);
-        mb = fmaxf(mb, x[(h ^ 1) * 384 + 256]);
-        if (rv) {
-          if (h == 0) {
-            p.sy[(size_t)n_blk * p.M + row] = fp8_scale<FP8_E4M3>(my);
-            if (p.out2 != nullptr) {
-              p.sab[(size_t)n_blk * p.M + row] = fp8_scale<FP8_E4M3>(ma);
-              p.sab[(size_t)(n_blk + p.split / 128) * p.M + row] = fp8_scale<FP8_E4M3>(mb);
+        for (int i = 0; i < 64; ++i) split(sums[i], acc[2 * i], acc[2 * i + 1]);
+        if constexpr (EPI == F8_EPI_BF16) {
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + (size_t)row * p.N + col0;
+#pragma unroll
+          for (int c = 0; c < 128; c += 16) {
+            if (!rv || col0 + c >= p.N) break;
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(acc[c + 2 * i], acc[c + 2 * i + 1]);
+            f8_store32(o + c, w, p.wide);
+          }
+        } else if constexpr (EPI == F8_EPI_F32) {
+          float* o = static_cast<float*>(p.out) + (size_t)row * p.N + col0;
+          if (p.add) {
+#pragma unroll
+            for (int c = 0; c < 128; c += 4) {
+              if (!rv || col0 + c >= p.N) break;
+              f8_add16(o + c, acc + c);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 128; c += 8) {
+              if (!rv || col0 + c >= p.N) break;
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(acc[c + i]);
+              f8_store32(o + c, w, p.wide);
             }
           }
-          const float fy = fp8_factor<FP8_E4M3>(my);
-          f8_store_row64(static_cast<uint8_t*>(p.out) + (size_t)row * p.N + col0, p.wide,
-                         [&](int i) { return acc[i] * sigmoid_f(acc[i]) * acc[64 + i] * fy; });
-          if (p.out2 != nullptr) {
-            const float fa = fp8_factor<FP8_E4M3>(ma), fb = fp8_factor<FP8_E4M3>(mb);
-            uint8_t* ab = static_cast<uint8_t*>(p.out2) + (size_t)row * 2 * p.N + col0;
-            f8_store_row64(ab, p.wide, [&](int i) { return acc[i] * fa; });
-            f8_store_row64(ab + p.split, p.wide, [&](int i) { return acc[64 + i] * fb; });
+        } else {
+          // Columns 0-63 are a, 64-127 the same columns of b.  One scale per row
+          // and 128 columns: the two halves exchange their maxima.
+          float my = 0.f, ma = 0.f, mb = 0.f;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            my = fmaxf(my, fabsf(acc[i] * sigmoid_f(acc[i]) * acc[64 + i]));
+            ma = fmaxf(ma, fabsf(acc[i]));
+            mb = fmaxf(mb, fabsf(acc[64 + i]));
+          }
+          float* x = sXch + (tiles_done & 1) * 768 + q * 32 + lane;
+          x[h * 384] = my;
+          x[h * 384 + 128] = ma;
+          x[h * 384 + 256] = mb;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(xch);
+          mbar_wait_drain(smem_u32(xch), tiles_done & 1u, wctl, (2 + q) << 8 | kWaitAccFull);
+          if (__any_sync(0xffffffffu, *abort_flag)) break;
+          my = fmaxf(my, x[(h ^ 1) * 384]);
+          ma = fmaxf(ma, x[(h ^ 1) * 384 + 128]);
+          mb = fmaxf(mb, x[(h ^ 1) * 384 + 256]);
+          if (rv) {
+            if (h == 0) {
+              p.sy[(size_t)n_blk * p.M + row] = fp8_scale<FP8_E4M3>(my);
+              if (p.out2 != nullptr) {
+                p.sab[(size_t)n_blk * p.M + row] = fp8_scale<FP8_E4M3>(ma);
+                p.sab[(size_t)(n_blk + p.split / 128) * p.M + row] = fp8_scale<FP8_E4M3>(mb);
+              }
+            }
+            const float fy = fp8_factor<FP8_E4M3>(my);
+            f8_store_row64(static_cast<uint8_t*>(p.out) + (size_t)row * p.N + col0, p.wide,
+                           [&](int i) { return acc[i] * sigmoid_f(acc[i]) * acc[64 + i] * fy; });
+            if (p.out2 != nullptr) {
+              const float fa = fp8_factor<FP8_E4M3>(ma), fb = fp8_factor<FP8_E4M3>(mb);
+              uint8_t* ab = static_cast<uint8_t*>(p.out2) + (size_t)row * 2 * p.N + col0;
+              f8_store_row64(ab, p.wide, [&](int i) { return acc[i] * fa; });
+              f8_store_row64(ab + p.split, p.wide, [&](int i) { return acc[64 + i] * fb; });
+            }
           }
         }
       }
