@@ -159,6 +159,26 @@ __device__ __forceinline__ float max16(float v) {
   return v;
 }
 
+// Larger of two pairs of bf16 (a NaN beside a number is left out).
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// 8 bf16 times 8 factors (or one), as 8-bit values.
+template <int FMT>
+__device__ __forceinline__ uint2 fp8_pack8(const uint4& q, const F2 (&f)[4]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    split(f2(bf16lo(w[i]), bf16hi(w[i])) * f[i], lo, hi);
+    r[i] = fp8_pack2<FMT>(lo, hi);
+  }
+  return make_uint2(r[0] | r[1] << 16, r[2] | r[3] << 16);
+}
+
 // ------------------------------------------------------------------ quantiser
 
 // One CTA per 128 x 128 tile, read once: a thread holds 8 columns of 8 rows
@@ -199,6 +219,50 @@ __global__ void __launch_bounds__(kQuantThreads, 4) quant_fp8_kernel(const Quant
     const int row = r0 + 16 * i;
     x[i] = (cv && row < p.R) ? ldg_nc_v4(p.x + t0 + (o0 + (uint32_t)(16 * i) * p.C)) : make_uint4(0u, 0u, 0u, 0u);
   }
+  // Without VEC the maxima are taken of the bf16 values, two to a word.
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  uint32_t cm[4] = {0u, 0u, 0u, 0u};  // columns, then the tile
+  if constexpr (!VEC) {
+    uint32_t rm[kQuantRows];
+#pragma unroll
+    for (int i = 0; i < kQuantRows; ++i) {
+      const uint32_t w[4] = {x[i].x & kAbs, x[i].y & kAbs, x[i].z & kAbs, x[i].w & kAbs};
+      if constexpr (COLS || BLOCKS) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cm[j] = max_bf16x2(cm[j], w[j]);
+      }
+      if constexpr (ROWS) rm[i] = max_bf16x2(max_bf16x2(max_bf16x2(0u, w[0]), w[1]), max_bf16x2(max_bf16x2(0u, w[2]), w[3]));
+    }
+    if constexpr (ROWS) {
+      // Rows 2 t and 2 t + 1 to word t; then the 16 lanes halve what they hold:
+      // lane l ends with word l / 4, and takes the row l % 2 of it.
+      static_assert(kQuantRows == 8, "8 rows over 16 lanes");
+      uint32_t m[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        m[t] = max_bf16x2(__byte_perm(rm[2 * t], rm[2 * t + 1], 0x5410), __byte_perm(rm[2 * t], rm[2 * t + 1], 0x7632));
+      const bool up8 = lane & 8, up4 = lane & 4;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up8 ? m[t] : m[t + 2], 8);
+        m[t] = max_bf16x2(up8 ? m[t + 2] : m[t], got);
+      }
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, up4 ? m[0] : m[1], 4);
+      uint32_t w = max_bf16x2(up4 ? m[1] : m[0], got);
+      w = max_bf16x2(w, __shfl_xor_sync(0xffffffffu, w, 2));
+      w = max_bf16x2(w, __shfl_xor_sync(0xffffffffu, w, 1));
+      const float amax = lane & 1 ? bf16hi(w) : bf16lo(w);
+      const int mine = r0 + 16 * (lane % 16 / 4 * 2 + (lane & 1));
+      if (!(lane & 2) && mine < p.R) p.sr[(size_t)tc * p.R + mine] = fp8_scale<FMT>(amax);
+      const float factor = fp8_factor<FMT>(amax);
+#pragma unroll
+      for (int i = 0; i < kQuantRows; ++i) {
+        const float fr = __shfl_sync(0xffffffffu, factor, (lane & 16) | (i / 2 * 4) | (i & 1));
+        const F2 f[4] = {f2(fr, fr), f2(fr, fr), f2(fr, fr), f2(fr, fr)};
+        if (cv && r0 + 16 * i < p.R) stg_v2(p.qr + t0 + (o0 + (uint32_t)(16 * i) * p.C), fp8_pack8<FMT>(x[i], f));
+      }
+    }
+  }
   float cvec[8], rvec[kQuantRows];
   if constexpr (VEC) {
 #pragma unroll
@@ -212,40 +276,38 @@ __global__ void __launch_bounds__(kQuantThreads, 4) quant_fp8_kernel(const Quant
   }
   auto values = [&](int i, float* f) {
     unpack8(x[i], f);
-    if constexpr (VEC) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = f[j] * rvec[i] * cvec[j];
-    }
+    for (int j = 0; j < 8; ++j) f[j] = f[j] * rvec[i] * cvec[j];
   };
   float cmax[8];
+  if constexpr (VEC) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) cmax[j] = 0.f;
+    for (int j = 0; j < 8; ++j) cmax[j] = 0.f;
 #pragma unroll
-  for (int i = 0; i < kQuantRows; ++i) {
-    float f[8];
-    values(i, f);
-    float rmax = 0.f;
+    for (int i = 0; i < kQuantRows; ++i) {
+      float f[8];
+      values(i, f);
+      float rmax = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      rmax = fmaxf(rmax, fabsf(f[j]));
-      cmax[j] = fmaxf(cmax[j], fabsf(f[j]));
-    }
-    if constexpr (ROWS) {
-      rmax = max16(rmax);
-      const int row = r0 + 16 * i;
-      if (row < p.R) {
-        if (cv) stg_v2(p.qr + t0 + (o0 + (uint32_t)(16 * i) * p.C), fp8_pack8<FMT>(f, fp8_factor<FMT>(rmax)));
-        if (lane % 16 == 0) p.sr[(size_t)tc * p.R + row] = fp8_scale<FMT>(rmax);
+      for (int j = 0; j < 8; ++j) {
+        rmax = fmaxf(rmax, fabsf(f[j]));
+        cmax[j] = fmaxf(cmax[j], fabsf(f[j]));
+      }
+      if constexpr (ROWS) {
+        rmax = max16(rmax);
+        const int row = r0 + 16 * i;
+        if (row < p.R) {
+          if (cv) stg_v2(p.qr + t0 + (o0 + (uint32_t)(16 * i) * p.C), fp8_pack8<FMT>(f, fp8_factor<FMT>(rmax)));
+          if (lane % 16 == 0) p.sr[(size_t)tc * p.R + row] = fp8_scale<FMT>(rmax);
+        }
       }
     }
   }
   if constexpr (COLS || BLOCKS) {
+    F2 fac[4];
     if constexpr (BLOCKS) {
-      float m = cmax[0];
-#pragma unroll
-      for (int j = 1; j < 8; ++j) m = fmaxf(m, cmax[j]);
-      m = max16(m);
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+      uint32_t w = max_bf16x2(max_bf16x2(cm[0], cm[1]), max_bf16x2(cm[2], cm[3]));
+      float m = warp_max(fmaxf(bf16lo(w), bf16hi(w)));
       if (lane == 0) smax[warp][0] = m;
       __syncthreads();
 #pragma unroll
@@ -253,10 +315,19 @@ __global__ void __launch_bounds__(kQuantThreads, 4) quant_fp8_kernel(const Quant
       if (threadIdx.x == 0) p.sc[(size_t)tr * p.tiles_c + tc] = fp8_scale<FMT>(m);
       m = fp8_factor<FMT>(m);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) cmax[j] = m;
+      for (int j = 0; j < 4; ++j) fac[j] = f2(m, m);
     } else {
+      if constexpr (!VEC) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) cmax[j] = fmaxf(cmax[j], __shfl_xor_sync(0xffffffffu, cmax[j], 16));
+        for (int j = 0; j < 4; ++j) {
+          cm[j] = max_bf16x2(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 16));
+          cmax[2 * j] = bf16lo(cm[j]);
+          cmax[2 * j + 1] = bf16hi(cm[j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) cmax[j] = fmaxf(cmax[j], __shfl_xor_sync(0xffffffffu, cmax[j], 16));
+      }
       if (lane < 16) sts8(&smax[warp][lane * 8], cmax);
       __syncthreads();
       if (threadIdx.x < 128) {  // one column each: maximum, scale, factor
@@ -269,16 +340,23 @@ __global__ void __launch_bounds__(kQuantThreads, 4) quant_fp8_kernel(const Quant
       }
       __syncthreads();
       lds8(&sfac[(lane % 16) * 8], cmax);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) fac[j] = f2(cmax[2 * j], cmax[2 * j + 1]);
     }
 #pragma unroll
     for (int i = 0; i < kQuantRows; ++i) {
-      const int row = r0 + 16 * i;
-      float f[8];
+      if (!cv || r0 + 16 * i >= p.R) continue;
       forget(x[i]);
-      values(i, f);
+      uint8_t* dst = p.qc + t0 + (o0 + (uint32_t)(16 * i) * p.C);
+      if constexpr (VEC) {
+        float f[8];
+        values(i, f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] *= cmax[j];
-      if (cv && row < p.R) stg_v2(p.qc + t0 + (o0 + (uint32_t)(16 * i) * p.C), fp8_pack8<FMT>(f, 1.f));
+        for (int j = 0; j < 8; ++j) f[j] *= cmax[j];
+        stg_v2(dst, fp8_pack8<FMT>(f, 1.f));
+      } else {
+        stg_v2(dst, fp8_pack8<FMT>(x[i], fac));
+      }
     }
   }
 }
