@@ -165,18 +165,23 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// 8 bf16 times 8 factors (or one), as 8-bit values.
+// 8 values times their factors, as 8-bit values.
 template <int FMT>
-__device__ __forceinline__ uint2 fp8_pack8(const uint4& q, const F2 (&f)[4]) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+__device__ __forceinline__ uint2 fp8_pack8(const F2 (&v)[4], const F2 (&f)[4]) {
   uint32_t r[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float lo, hi;
-    split(f2(bf16lo(w[i]), bf16hi(w[i])) * f[i], lo, hi);
+    split(v[i] * f[i], lo, hi);
     r[i] = fp8_pack2<FMT>(lo, hi);
   }
   return make_uint2(r[0] | r[1] << 16, r[2] | r[3] << 16);
+}
+template <int FMT>
+__device__ __forceinline__ uint2 fp8_pack8(const uint4& q, const F2 (&f)[4]) {
+  const F2 v[4] = {f2(bf16lo(q.x), bf16hi(q.x)), f2(bf16lo(q.y), bf16hi(q.y)), f2(bf16lo(q.z), bf16hi(q.z)),
+                   f2(bf16lo(q.w), bf16hi(q.w))};
+  return fp8_pack8<FMT>(v, f);
 }
 
 // ------------------------------------------------------------------ quantiser
@@ -200,7 +205,7 @@ struct QuantParams {
 };
 
 template <int FMT, bool ROWS, bool COLS, bool BLOCKS, bool VEC>
-__global__ void __launch_bounds__(kQuantThreads, 4) quant_fp8_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kQuantThreads, VEC ? 3 : 4) quant_fp8_kernel(const QuantParams p) {
   __shared__ __align__(16) float smax[kQuantThreads / 32][128];
   __shared__ __align__(16) float sfac[128];
   griddep_wait();
@@ -263,42 +268,54 @@ __global__ void __launch_bounds__(kQuantThreads, 4) quant_fp8_kernel(const Quant
       }
     }
   }
-  float cvec[8], rvec[kQuantRows];
+  F2 cvec[4];
+  float rvec[kQuantRows];
   if constexpr (VEC) {
+    float c[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    if (p.colvec != nullptr && cv) unpack8(ldg_nc_v4_l1(p.colvec + c0), c);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) cvec[j] = 1.f;
-    if (p.colvec != nullptr && cv) unpack8(ldg_nc_v4_l1(p.colvec + c0), cvec);
+    for (int j = 0; j < 4; ++j) cvec[j] = f2(c[2 * j], c[2 * j + 1]);
 #pragma unroll
     for (int i = 0; i < kQuantRows; ++i) {
       const int row = r0 + 16 * i;
       rvec[i] = (p.rowvec != nullptr && row < p.R) ? p.rowvec[row] : 1.f;
     }
   }
-  auto values = [&](int i, float* f) {
-    unpack8(x[i], f);
+  auto values = [&](int i, F2 (&f)[4]) {
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = f[j] * rvec[i] * cvec[j];
+    for (int j = 0; j < 4; ++j) f[j] = f2(bf16lo(w[j]), bf16hi(w[j])) * f2(rvec[i], rvec[i]) * cvec[j];
   };
   float cmax[8];
   if constexpr (VEC) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) cmax[j] = 0.f;
 #pragma unroll
-    for (int i = 0; i < kQuantRows; ++i) {
-      float f[8];
-      values(i, f);
-      float rmax = 0.f;
+    for (int i = 0; i < kQuantRows; i += 2) {
+      F2 f[2][4];
+      float v[2][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        rmax = fmaxf(rmax, fabsf(f[j]));
-        cmax[j] = fmaxf(cmax[j], fabsf(f[j]));
+      for (int k = 0; k < 2; ++k) {
+        values(i + k, f[k]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split(f[k][j], v[k][2 * j], v[k][2 * j + 1]);
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) cmax[j] = max3_abs(cmax[j], v[0][j], v[1][j]);
       if constexpr (ROWS) {
-        rmax = max16(rmax);
-        const int row = r0 + 16 * i;
-        if (row < p.R) {
-          if (cv) stg_v2(p.qr + t0 + (o0 + (uint32_t)(16 * i) * p.C), fp8_pack8<FMT>(f, fp8_factor<FMT>(rmax)));
-          if (lane % 16 == 0) p.sr[(size_t)tc * p.R + row] = fp8_scale<FMT>(rmax);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float rmax = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) rmax = max3_abs(rmax, v[k][j], v[k][j + 1]);
+          rmax = max16(rmax);
+          const int row = r0 + 16 * (i + k);
+          if (row < p.R) {
+            const float fr = fp8_factor<FMT>(rmax);
+            const F2 factor[4] = {f2(fr, fr), f2(fr, fr), f2(fr, fr), f2(fr, fr)};
+            if (cv) stg_v2(p.qr + t0 + (o0 + (uint32_t)(16 * (i + k)) * p.C), fp8_pack8<FMT>(f[k], factor));
+            if (lane % 16 == 0) p.sr[(size_t)tc * p.R + row] = fp8_scale<FMT>(rmax);
+          }
         }
       }
     }
@@ -349,11 +366,9 @@ __global__ void __launch_bounds__(kQuantThreads, 4) quant_fp8_kernel(const Quant
       forget(x[i]);
       uint8_t* dst = p.qc + t0 + (o0 + (uint32_t)(16 * i) * p.C);
       if constexpr (VEC) {
-        float f[8];
+        F2 f[4];
         values(i, f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] *= cmax[j];
-        stg_v2(dst, fp8_pack8<FMT>(f, 1.f));
+        stg_v2(dst, fp8_pack8<FMT>(f, fac));
       } else {
         stg_v2(dst, fp8_pack8<FMT>(x[i], fac));
       }
