@@ -34,10 +34,11 @@ bool operand8_map(CUtensorMap* m, const void* p, long long mn, long long k, bool
 }
 
 // Few rows of A: the weight becomes the MMA's 128-row operand, the rows its
-// columns (gemm_fp8_skinny_kernel).  Measured at N = K = 4096: 16 rows 6.9 us,
-// 64 rows 9.5 us, where a 256 x 256 tile is mostly padding (17 us); at 128 rows
-// the other way round (30 us).  The gate/up product holds two accumulators and
-// changes over at half the rows (64 rows, K = 4096, F = 11008: 69 us against 35).
+// columns (gemm_fp8_skinny_kernel).  Measured at N = K = 4096: 16 rows 6.8 us,
+// 64 rows 9.5 us, where the 256 x 256 tiles, mostly padding, take 16.5 us (65 to
+// 256 rows alike).  With 128 columns the few-rows form took 30 us there.  The
+// gate/up product holds two accumulators and changes over at half the rows (K
+// 4096, F 11008: 64 rows 69 us in the few-rows form, 34 us in tiles).
 inline int skinny8_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 
 // Rasterisation as pick_group, in bytes of 8-bit operands.
@@ -114,7 +115,7 @@ coda_status launch_skinny8(const CUtensorMap& tw, const CUtensorMap& tx, Skinny8
     ready[dev].store(true);
   }
   const int tiles = cdiv(p.N, 128);
-  int splits = 1;
+  int splits = 1;  // doubled while there are two CTAs per SM to be had and two blocks of k for each
   while (splits < 8 && tiles * splits * 2 <= 2 * g_dev[dev].num_sms && splits * 4 <= p.k_blocks) splits *= 2;
   p.idesc = (p.idesc & ~(0x3Fu << 17)) | ((uint32_t)(TN >> 3) << 17);
   p.wait_limit_ns = g_wait_limit_ns.load();
@@ -152,6 +153,10 @@ coda_status quant8(const QuantParams& p, bool rows, bool cols, bool vec, int gri
   return launch_pass(tag, quant_fp8_kernel<FMT, false, true, false, false>, grid, kQuantThreads, stream, p);
 }
 
+// A row over 256 threads from d = 1025 up: fewer threads of more columns leave
+// too few loads in flight per SM, more of them wait for one another (8192 rows;
+// 128, 256 and 512 threads: d = 2048 23.6, 22.1 us, -; d = 4096 42.6, 40.0, 42.1
+// us; d = 8192 -, 76.5, 80.6 us).  Wider rows need the registers of more threads.
 template <int T, int CH>
 coda_status rms8_fwd(const RmsParams& p, void* stream) {
   return launch_pass(CODA_KERNEL_RMSNORM_FP8_FWD, rmsnorm_fp8_fwd_kernel<T, CH>, p.M, T, stream, p);
@@ -160,9 +165,10 @@ coda_status rms8_fwd(const RmsParams& p, void* stream) {
 // Widest row the norms hold in registers.
 constexpr int kRms8MaxD = 1024 * 4 * 8;
 
-// Threads per row of the norm's backward (8 columns each up to d = 8192), and
-// its CTAs: a thousand threads per SM, each CTA keeping its share of dg in
-// registers and writing one partial row.
+// Threads per row of the norm's backward (8 columns each up to d = 8192: with 16
+// columns the next row's loads no longer fit in registers, 67 us against 45 for
+// 8192 x 4096 in L2-warm runs), and its CTAs: a thousand threads per SM, each
+// CTA keeping its share of dg in registers and writing one partial row.
 int rms8_bwd_threads(int d) { return d <= 1024 ? 128 : d <= 2048 ? 256 : d <= 4096 ? 512 : 1024; }
 int rms8_bwd_ctas(int M, int d) { return std::min(M, 148 * (1024 / rms8_bwd_threads(d))); }
 
