@@ -51,50 +51,81 @@ int pick_group8(long long a_rows, long long b_rows, int num_m, int num_n, int k_
   return -(int)std::min<long long>(num_n, g);
 }
 
-template <int EPI, bool A_MN, bool B_MN, bool VEC>
-coda_status launch_gemm8(const CUtensorMap& ta, const CUtensorMap& tb, Gemm8Params p, cudaStream_t s) {
-  static std::atomic<int> clusters_of[kMaxDevices];  // 0: not set up on this device yet
+// Clusters of 2 * parts CTAs of a kernel that the device holds at once.
+template <int EPI, bool A_MN, bool B_MN, bool VEC, bool SPLIT>
+coda_status gemm8_clusters(int parts, int& clusters) {
+  static std::atomic<int> of[kMaxDevices][5];  // 0: not set up on this device yet
   int dev = 0;
-  coda_status st = current_device(dev);
-  if (st != CODA_OK) return st;
-  auto kern = gemm_fp8_kernel<EPI, A_MN, B_MN, VEC>;
-  int clusters = clusters_of[dev].load();
+  CODA_TRY(current_device(dev));
+  auto kern = gemm_fp8_kernel<EPI, A_MN, B_MN, VEC, SPLIT>;
+  clusters = of[dev][parts].load();
   if (clusters == 0) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F8_SMEM_BYTES) != cudaSuccess)
       return CODA_ERR_CUDA;
-    clusters = g_dev[dev].num_sms / 2;
+    clusters = g_dev[dev].num_sms / (2 * parts);
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = 2 * parts;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(2 * clusters, 1, 1);
+    cfg.gridDim = dim3(2 * parts * clusters, 1, 1);
     cfg.blockDim = dim3(F8_THREADS, 1, 1);
     cfg.dynamicSmemBytes = F8_SMEM_BYTES;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0) clusters = std::min(clusters, n);
-    clusters_of[dev].store(clusters);
+    of[dev][parts].store(clusters);
   }
+  return CODA_OK;
+}
+
+template <int EPI, bool A_MN, bool B_MN, bool VEC, bool SPLIT = false>
+coda_status launch_gemm8(const CUtensorMap& ta, const CUtensorMap& tb, Gemm8Params p, cudaStream_t s, int parts = 1) {
+  auto kern = gemm_fp8_kernel<EPI, A_MN, B_MN, VEC, SPLIT>;
+  int clusters = 0;
+  CODA_TRY((gemm8_clusters<EPI, A_MN, B_MN, VEC, SPLIT>(parts, clusters)));
   p.wait_limit_ns = g_wait_limit_ns.load();
-  p.kernel_id = 0x40 + (uint32_t)(EPI * 8 + (A_MN ? 4 : 0) + (B_MN ? 2 : 0) + (VEC ? 1 : 0));
+  p.kernel_id = 0x40 + (uint32_t)(EPI * 8 + (A_MN ? 4 : 0) + (B_MN ? 2 : 0) + (VEC ? 1 : 0)) + (SPLIT ? 0x40 : 0);
   const long long tiles = (long long)p.num_m_tiles * p.num_n_tiles;
-  const int units = (int)std::min<long long>(tiles, clusters);
+  const int units = SPLIT ? (int)tiles : (int)std::min<long long>(tiles, clusters);
   g_launch_tag = EPI == F8_EPI_SWIGLU ? CODA_KERNEL_GEMM_SWIGLU_FP8 : CODA_KERNEL_GEMM_FP8;
-  const cudaError_t e =
-      launch_ex(kern, dim3(2 * units), dim3(F8_THREADS), F8_SMEM_BYTES, s, 2, ta, tb, p);
+  const cudaError_t e = launch_ex(kern, dim3(2 * parts * units), dim3(F8_THREADS), F8_SMEM_BYTES, s, 2 * parts, ta, tb, p);
   g_launch_tag = -1;
   return e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess ? CODA_OK : CODA_ERR_CUDA;
+}
+
+// An activation's product with a weight: when its tiles leave pairs idle, the
+// reduction of each is shared by 2 to 4 of them, as many as the device holds at
+// once.  The exchange costs 4 to 5 us, a block of k 0.4: it is done where a pair
+// is spared 12 blocks.  Measured without and with it, N = 2048: 256 rows (4
+// pairs), K 2048 11.1 and 10.7 us, K 8192 29.1 and 16.2; 1001 rows (32 tiles, 2
+// pairs), K 4096 17.9 and 16.7, K 16384 52.8 and 36.3; below the limit, K 2688
+// 13.8 and 14.7.
+// Weight gradients have a tile per 256 x 256 of the weight and fill the device.
+template <int EPI, bool B_MN>
+coda_status launch_gemm8_activation(const CUtensorMap& ta, const CUtensorMap& tb, const Gemm8Params& p, cudaStream_t s) {
+  const long long tiles = (long long)p.num_m_tiles * p.num_n_tiles;
+  for (int parts = 4; parts > 1; --parts) {
+    if (tiles * 2 * parts > num_sms() || p.k_blocks - cdiv(p.k_blocks, parts) < 12) continue;
+    int clusters = 0;
+    CODA_TRY((gemm8_clusters<EPI, false, B_MN, false, true>(parts, clusters)));
+    if (tiles <= clusters) return launch_gemm8<EPI, false, B_MN, false, true>(ta, tb, p, s, parts);
+  }
+  return launch_gemm8<EPI, false, B_MN, false>(ta, tb, p, s);
 }
 
 template <int EPI, bool VEC>
 coda_status launch_gemm8_majors(const CUtensorMap& ta, const CUtensorMap& tb, bool a_mn, bool b_mn,
                                 const Gemm8Params& p, cudaStream_t s) {
-  if (!a_mn && !b_mn) return launch_gemm8<EPI, false, false, VEC>(ta, tb, p, s);
-  if (!a_mn && b_mn) return launch_gemm8<EPI, false, true, VEC>(ta, tb, p, s);
+  if constexpr (!VEC) {
+    if (!a_mn) return b_mn ? launch_gemm8_activation<EPI, true>(ta, tb, p, s) : launch_gemm8_activation<EPI, false>(ta, tb, p, s);
+  } else {
+    if (!a_mn && !b_mn) return launch_gemm8<EPI, false, false, VEC>(ta, tb, p, s);
+    if (!a_mn && b_mn) return launch_gemm8<EPI, false, true, VEC>(ta, tb, p, s);
+  }
   if (a_mn && b_mn) return launch_gemm8<EPI, true, true, VEC>(ta, tb, p, s);
   return launch_gemm8<EPI, true, false, VEC>(ta, tb, p, s);
 }

@@ -350,7 +350,86 @@ __device__ __forceinline__ void f8_store_row64(uint8_t* dst, bool wide, Value va
   }
 }
 
-template <int EPI, bool A_MN, bool B_MN, bool VEC>
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+// Arrive on the barrier at this offset in the CTAs of `mask` when this thread's pair MMAs so far are complete.
+__device__ __forceinline__ void umma_commit_pair_mask(const uint64_t* bar, uint32_t mask) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                   smem_u32(bar)),
+               "h"((uint16_t)mask)
+               : "memory");
+}
+
+// With SPLIT the reduction of a tile is shared by the pairs of a cluster (2 to 4;
+// few tiles, long reductions): each pair takes a range of the blocks, leaves its
+// fp32 partial tile in its own shared memory, where the operands were, and then
+// finishes a share of the rows, adding the partials in the pairs' order and
+// reading the others' through distributed shared memory, whole rows at a time
+// (sent there from the drain, a row per thread, they took twice as long).  One
+// tile per cluster.
+constexpr int F8_PART_PITCH = (256 + 4) * 4;  // bytes per row of a partial tile: rows 16 bytes apart in the banks
+static_assert(128 * F8_PART_PITCH <= F8_STAGES * F8_STAGE_BYTES, "the partial tile takes the ring's place");
+
+// The second half of a SPLIT tile, by the drain warps: this pair's share of the
+// rows, 64 threads to a row.
+template <int EPI>
+__device__ __forceinline__ void f8_finish_share(const Gemm8Params& p, const uint8_t* smem) {
+  // Read again rather than kept: the drain has no registers to spare.
+  const int crank = (int)cluster_ctarank(), part = crank / 2, parts = (int)cluster_nctarank() / 2;
+  int m_blk, n_blk;
+  tile_coords((int)cluster_id_x(), p.num_m_tiles, p.num_n_tiles, p.group_m, m_blk, n_blk);
+  const int t = (int)threadIdx.x - 128;
+  const int col = n_blk * 256 + t % 64 * 4, m0 = m_blk * 256 + crank % 2 * 128;
+  const int end = min((part + 1) * 128 / parts, p.M - m0);
+  const uint8_t* own = smem + t % 64 * 16;
+  uint32_t from[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) from[j] = mapa_shared(smem_u32(own), (uint32_t)(min(j, parts - 1) * 2 + crank % 2));
+  if (col < p.N) {
+#pragma unroll 2
+    for (int r = part * 128 / parts + t / 64; r < end; r += 4) {
+      float4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j == part) v[j] = *reinterpret_cast<const float4*>(own + r * F8_PART_PITCH);
+        else if (j < parts) v[j] = ld_cluster_f32x4(from[j] + r * F8_PART_PITCH);
+      }
+      float f[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int j = 1; j < 4; ++j) {
+        f[0] += v[j].x;
+        f[1] += v[j].y;
+        f[2] += v[j].z;
+        f[3] += v[j].w;
+      }
+      const size_t o = (size_t)(m0 + r) * p.N + col;
+      if constexpr (EPI == F8_EPI_BF16) {
+        stg_v2(static_cast<__nv_bfloat16*>(p.out) + o, make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])));
+      } else if (p.add) {
+        f8_add16(static_cast<float*>(p.out) + o, f);
+      } else {
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = make_float4(f[0], f[1], f[2], f[3]);
+      }
+    }
+  }
+}
+
+template <int EPI, bool A_MN, bool B_MN, bool VEC, bool SPLIT>
 __global__ void __launch_bounds__(F8_THREADS, 1)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const Gemm8Params p) {
@@ -377,7 +456,16 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0);  // known uniform
   const int lane = threadIdx.x % 32;
-  const uint32_t rank = cluster_ctarank();  // 0 = the pair's leader
+  static_assert(!SPLIT || (EPI != F8_EPI_SWIGLU && !VEC), "split products");
+  const uint32_t rank = SPLIT ? cluster_ctarank() & 1 : cluster_ctarank();  // 0 = the pair's leader
+  const uint32_t leader = SPLIT ? cluster_ctarank() & ~1u : 0u;             // its rank in the cluster
+  // This pair's 128-deep blocks.
+  int kb0 = 0, num_kb = p.k_blocks;
+  if constexpr (SPLIT) {
+    const int parts = (int)cluster_nctarank() / 2, part = (int)leader / 2;
+    kb0 = (int)((long long)part * p.k_blocks / parts);
+    num_kb = (int)((long long)(part + 1) * p.k_blocks / parts) - kb0;
+  }
   const int first_tile = (int)cluster_id_x();
   const int tile_step = (int)num_clusters_x();
 
@@ -429,16 +517,16 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         int m_blk, n_blk;
         tile_coords(tile, p.num_m_tiles, p.num_n_tiles, p.group_m, m_blk, n_blk);
         const int a_row = m_blk * 256 + (int)rank * 128;
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
+        for (int kb = 0; kb < num_kb; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, ctl, 0, kWaitEmpty)) {
             ok = false;
             break;
           }
           uint8_t* a_dst = sA + stage * F8_A_BYTES;
           uint8_t* b_dst = sB + stage * F8_B_BYTES;
-          const int k0 = kb * F8_BK;
+          const int k0 = (kb0 + kb) * F8_BK;
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * F8_STAGE_BYTES);
-          const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+          const uint32_t bar = mapa_shared(smem_u32(&full[stage]), leader);
           if constexpr (A_MN) tma_load_2d_pair(a_dst, &tmA, bar, a_row, k0, hint);
           else tma_load_2d_pair(a_dst, &tmA, bar, k0, a_row, hint);
 #pragma unroll
@@ -471,7 +559,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                                half * (8192 >> 4);
       for (int tile = first_tile; tile < num_tiles; tile += tile_step) {
 #pragma unroll 1
-        for (int kb = p.k_blocks; kb > 0; --kb, ++it) {
+        for (int kb = num_kb; kb > 0; --kb, ++it) {
           const uint32_t buf = (it & 1) * 2 + half;
           mbar_wait_drain(full_s + stage * 8, phase, wctl, 1 << 8 | kWaitFull);
           mbar_wait_drain(smem_u32(tempty) + buf * 8, ((it >> 1) & 1u) ^ 1u, wctl, 1 << 8 | kWaitAccEmpty);
@@ -481,8 +569,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
           umma_f8_stage_pair<A_MN ? 256 : 2, B_MN ? 128 : 2>(
               tmem_base + buf * 128, a_desc0 + (uint64_t)(stage * (F8_A_BYTES >> 4)),
               b_desc0 + (uint64_t)(stage * (F8_B_BYTES >> 4)), p.idesc);
-          umma_commit_pair_both(&tfull[buf]);
-          umma_commit_pair_both(&empty[stage]);  // with the other half's: both CTAs' operand tiles have been read
+          if constexpr (SPLIT) umma_commit_pair_mask(&tfull[buf], 3u << leader);
+          else umma_commit_pair_both(&tfull[buf]);
+          if constexpr (SPLIT) umma_commit_pair_mask(&empty[stage], 3u << leader);
+          else umma_commit_pair_both(&empty[stage]);  // with the other half's: both CTAs' operand tiles have been read
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
@@ -490,7 +580,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         }
         if (*abort_flag) break;
       }
-      umma_commit_pair(mapa_shared(smem_u32(mma_done), 0));
+      umma_commit_pair(mapa_shared(smem_u32(mma_done), leader));
       mbar_wait_own(mma_done, 0, ctl.limit_ns);
     } else if (warp == 2) {
       // ---------------------------------------------------------------- scales (both CTAs)
@@ -502,8 +592,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         tile_coords(tile, p.num_m_tiles, p.num_n_tiles, p.group_m, m_blk, n_blk);
         // This lane's rows (32 apart) and columns, and which of them exist.
         const int row = m_blk * 256 + (int)rank * 128 + lane;
-        const float* sa = p.sa + row;
-        const float* sb = p.sb;
+        const float* sa = p.sa + (size_t)kb0 * p.M + row;
+        const float* sb = p.sb + (size_t)kb0 * p.sb_k;
         int b_ok = 0;
         if constexpr (VEC) {
           sb += n_blk * 256 + lane * 4;
@@ -513,7 +603,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
           b_ok = EPI == F8_EPI_SWIGLU || nb * 128 < p.N;
           sb += (size_t)nb * p.sb_n;
         }
-        for (int left = p.k_blocks; left > 0; left -= F8_GROUP) {
+        for (int left = num_kb; left > 0; left -= F8_GROUP) {
           ok = __all_sync(0xffffffffu, mbar_wait(&sempty[st], phase ^ 1u, ctl, 6, kWaitEmpty));
           if (!ok) break;
           uint32_t dst = smem_u32(sScale + st * GROUP_FLOATS) + lane * 4;
@@ -543,6 +633,11 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
+    if constexpr (SPLIT) {
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     // ---------------------------------------------------------------- drain and epilogue (both CTAs)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F8_REGS_DRAIN));
@@ -552,9 +647,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     const uint32_t wctl = smem_u32(drain_ctl);
     // Buffers of parity 0; parity 1 is 16 bytes and 256 columns on (bits that are 0 here).
     uint32_t tfull_h = smem_u32(&tfull[h]);
-    uint32_t tempty_h = mapa_shared(smem_u32(&tempty[h]), 0);
+    uint32_t tempty_h = mapa_shared(smem_u32(&tempty[h]), leader);
     uint32_t taddr_h = tmem_base + (uint32_t)(h * 128) + ((uint32_t)(q * 32) << 16);
     uint32_t it = 0, groups = 0, tiles_done = 0;
+    bool given = false;  // SPLIT: the partial tile is in shared memory
     for (int tile = first_tile; tile < num_tiles; tile += tile_step, ++tiles_done) {
       int m_blk, n_blk;
       tile_coords(tile, p.num_m_tiles, p.num_n_tiles, p.group_m, m_blk, n_blk);
@@ -566,7 +662,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
 #pragma unroll
       for (int i = 0; i < 64; ++i) sums[i] = F2{0};
 #pragma unroll 1
-      for (int left = p.k_blocks; left > 0; left -= F8_GROUP, ++groups) {
+      for (int left = num_kb; left > 0; left -= F8_GROUP, ++groups) {
         mbar_wait_drain(smem_u32(&sfull[groups & 1]), (groups >> 1) & 1u, wctl, (2 + q) << 8 | kWaitFull);
         if (*abort_flag) break;
         const float* sc = sScale + (groups & 1) * GROUP_FLOATS;
@@ -614,7 +710,18 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         mbar_arrive_if(smem_u32(&sempty[groups & 1]), one);
       }
       if (__any_sync(0xffffffffu, *abort_flag)) break;  // some block above may not have been complete
-      if constexpr (VEC) {
+      if constexpr (SPLIT) {
+        cluster_sync();  // both halves' MMAs have read the operands
+        given = true;
+        uint8_t* dst = smem + (q * 32 + lane) * F8_PART_PITCH + h * 512;
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+          float4 v;
+          split(sums[i], v.x, v.y);
+          split(sums[i + 1], v.z, v.w);
+          *reinterpret_cast<float4*>(dst + 8 * i) = v;
+        }
+      } else if constexpr (VEC) {
         // Four lanes hold 8 neighbouring columns of a row.
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -709,6 +816,11 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
           }
         }
       }
+    }
+    if constexpr (SPLIT) {
+      if (!given) cluster_sync();
+      cluster_sync();  // all partial tiles are there
+      if (!*abort_flag) f8_finish_share<EPI>(p, smem);
     }
   }
 
@@ -808,12 +920,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
       : "memory");
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-  return v;
-}
-
 // Sum of the cluster's copies of one partial, in rank order; the loads are in flight together.
 __device__ __forceinline__ float f8_cluster_sum(uint32_t addr, int splits) {
   float v[8];
@@ -848,8 +954,7 @@ __global__ void __launch_bounds__(F8S_THREADS, 2)
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0);
   const int lane = threadIdx.x % 32;
   const int rank = (int)cluster_ctarank();
-  int splits;
-  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(splits));
+  const int splits = (int)cluster_nctarank();
   const int n_blk = (int)blockIdx.x / splits;
   const int kb0 = (int)((long long)rank * p.k_blocks / splits);
   const int nkb = (int)((long long)(rank + 1) * p.k_blocks / splits) - kb0;

@@ -162,6 +162,34 @@ def test_gemm_few_rows(cuda_lib, M, N, K):
     assert torch.equal(one, cuda_lib.gemm_fp8(*args, **kw))
 
 
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("M,N,K,b_mn", [
+    (65, 256, 2048, False),     # 4 pairs of 4 blocks each
+    (129, 272, 2064, False),    # 17 blocks over 4 pairs, the last one short
+    (700, 1040, 4112, True),    # a short last tile both ways, MN-major weight
+    (257, 16, 4096, False),     # one row in the second tile, one tile of 16 columns
+    (4700, 256, 2320, False),   # 19 tiles: 3 pairs each, shares of 42 and 43 rows
+    (1001, 2048, 3344, True),   # 32 tiles: 2 pairs each
+])
+def test_gemm_reduction_shared_by_pairs(cuda_lib, M, N, K, b_mn, f32):
+    """Fewer tiles than pairs of SMs: the partial tiles are added in a fixed order, rows behind the last one are left."""
+    args, kw, ref, err = _gemm_case(cuda_lib, M, N, K, False, b_mn, True, "e4m3", "e5m2", f32, seed=M)
+    buf = torch.full((M + 300, N), 7.0, dtype=kw["out_dtype"], device="cuda")
+    ws = cuda_lib.Workspace(256)
+    cuda_lib.gemm_fp8(*args, **kw, out=buf[:M], ws=ws)
+    first = buf[:M].clone()
+    assert (buf[M:] == 7.0).all() and ws.query() == (0, 0)
+    check_close(num(first), ref, err if f32 else err + BF16 * (np.abs(ref) + err), "shared")
+    for _ in range(5):
+        assert _same(cuda_lib.gemm_fp8(*args, **kw), first)
+    if f32:
+        start = _randn(M, N, seed=3)
+        C = start.cuda()
+        cuda_lib.gemm_fp8(*args, **kw, accumulate=True, out=C)
+        want = num(start) + ref
+        check_close(num(C), want, err + FP32 * (np.abs(want) + err), "added")
+
+
 @pytest.mark.parametrize("K", [1, 2, 127, 128, 129, 1000])
 def test_gemm_any_reduction_for_weight_gradients(cuda_lib, K):
     args, kw, ref, err = _gemm_case(cuda_lib, 272, 400, K, True, True, False, "e5m2", "e4m3", True, seed=K)
