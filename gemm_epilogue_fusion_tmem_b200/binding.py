@@ -751,15 +751,19 @@ def _status_workspace(dev) -> Workspace:
     return ws
 
 
-def fp8_status(device=None) -> tuple[int, int]:
+def fp8_status(device=None, clear: bool = False) -> tuple[int, int]:
     """Synchronise the current stream and return (status, detail) of the 8-bit
     products that were given no workspace on this device (but for those captured
-    into a graph before the first eager one)."""
+    into a graph before the first eager one).  An error stays until `clear`."""
     dev = torch.device("cuda" if device is None else device)
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
     with torch.cuda.device(dev):
-        return _status_workspace(dev).query()
+        ws = _status_workspace(dev)
+        status = ws.query()
+        if clear:
+            ws.clear()
+        return status
 
 
 def quant_fp8(X, rows: bool = True, cols: bool = False, rowvec=None, colvec=None, fmt=torch.float8_e4m3fn,

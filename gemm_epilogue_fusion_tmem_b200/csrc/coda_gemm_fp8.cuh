@@ -379,8 +379,8 @@ __device__ __forceinline__ void umma_commit_pair_mask(const uint64_t* bar, uint3
 // fp32 partial tile in its own shared memory, where the operands were, and then
 // finishes a share of the rows, adding the partials in the pairs' order and
 // reading the others' through distributed shared memory, whole rows at a time
-// (sent there from the drain, a row per thread, they took twice as long).  One
-// tile per cluster.
+// (sent to the finisher from the drain, a row per thread: 45 us for 36 at 1001 x
+// 2048 x 16384).  One tile per cluster.
 constexpr int F8_PART_PITCH = (256 + 4) * 4;  // bytes per row of a partial tile: rows 16 bytes apart in the banks
 static_assert(128 * F8_PART_PITCH <= F8_STAGES * F8_STAGE_BYTES, "the partial tile takes the ring's place");
 

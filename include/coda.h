@@ -375,9 +375,9 @@ coda_status coda_qkv_rope_bwd(const void* dQKV, const void* X, const void* Wqkv,
  * a weight gradient dY^T X takes dY and X as they are stored, in columns form.
  *
  * Quantised matrices are dense, their column count a multiple of 16 (at most
- * 2^22 in the passes other than coda_gemm_fp8); any number of rows.  Outputs may not overlap inputs.  These calls allocate nothing and,
- * but for the norm's backward, need no scratch; `ws` of the two products holds
- * only the status word. */
+ * 2^22 in the passes other than coda_gemm_fp8); any number of rows.  Outputs may
+ * not overlap inputs.  These calls allocate nothing and, but for the norm's
+ * backward, need no scratch; `ws` of the two products holds only the status word. */
 #define CODA_FP8_E4M3 0
 #define CODA_FP8_E5M2 1
 
@@ -401,6 +401,8 @@ coda_status coda_quant_fp8_blocks(const void* W, void* Q, float* S, int R, int C
  * the tensor cores, scaled and added in fp32.  c_fp32 = 0: C bf16.  c_fp32 = 1: C fp32, and with
  * accumulate = 1 the product is added to C (gradient accumulation).
  * Requires N % 16 == 0; K % 16 == 0 unless both operands are MN-major; M % 16 == 0 when a_mn_major.
+ * The order of the additions depends on M, N, K and the device, not on the run; added sums below
+ * 2^-126 may be flushed to zero.
  * M = 0 or N = 0 does nothing; K = 0 writes zeros (adds nothing).  ws: coda_gemm_workspace_bytes(). */
 coda_status coda_gemm_fp8(const void* A, const float* SA, const void* B, const float* SB, void* C, int M, int N, int K,
                           int a_mn_major, int b_mn_major, int a_format, int b_format, int b_blocks, int c_fp32,

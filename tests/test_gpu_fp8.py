@@ -483,6 +483,14 @@ def test_first_call_inside_a_capture(cuda_lib):
     check_close(num(out), a @ b.T, gemm_error(a, b, 256), "captured")
 
 
+def test_status_stays_until_cleared(cuda_lib):
+    """The shared status word as a product that gave up would leave it (written here by the host)."""
+    word = cuda_lib._status_workspace(torch.device("cuda", torch.cuda.current_device())).buf.view(torch.int32)
+    word[0], word[1] = 7, 5
+    assert cuda_lib.fp8_status() == (7, 5) and cuda_lib.fp8_status("cuda", clear=True) == (7, 5)
+    assert cuda_lib.fp8_status("cuda:0") == (0, 0)
+
+
 def test_profile_hook_names_the_8_bit_kernels(cuda_lib):
     B = cuda_lib
     t = _mlp_inputs(130, 256, 128)
@@ -569,6 +577,37 @@ def test_products_on_two_streams_at_once(cuda_lib):
     for i, t in got:
         assert _same(t, want[i]), i
     assert B.fp8_status() == (0, 0)
+
+
+def test_shared_reductions_on_two_streams_and_in_a_graph(cuda_lib):
+    """Products whose tiles are shared by clusters of pairs, at once on two streams and replayed."""
+    B = cuda_lib
+    cases = [(200, 512, 2304), (300, 1040, 4112)]
+    calls, want = [], []
+    for M, N, K in cases:
+        x = B.quant_fp8(_bf(M, K, seed=M).cuda())
+        w = B.quant_fp8_blocks(_bf(N, K, seed=N).cuda())
+        calls.append(lambda x=x, w=w, M=M, N=N, K=K, **kw: B.gemm_fp8(x["Qr"], x["Sr"], w["Q"], w["S"], M, N, K, **kw))
+        want.append(calls[-1]())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for rep in range(10):
+        for i, c in enumerate(calls):
+            with torch.cuda.stream(streams[(rep + i) % 2]):
+                got.append((i, c()))
+    torch.cuda.synchronize()
+    for i, t in got:
+        assert _same(t, want[i]), i
+    outs = [torch.zeros_like(t) for t in want]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for c, o in zip(calls, outs):
+            c(out=o)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(_same(o, t) for o, t in zip(outs, want)) and B.fp8_status() == (0, 0)
 
 
 TAIL = 40  # rows checked at the end of a tensor of more than 2^32 elements
