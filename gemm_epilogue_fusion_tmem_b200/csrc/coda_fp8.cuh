@@ -33,10 +33,18 @@ struct IntC {
 };
 constexpr float kFp8Tiny = 7.888609052210118e-31f;  // 2^-100
 
-// Scale of a block and the factor its values are multiplied by.
+// Scale of a block and the factor its values are multiplied by, each the nearest
+// fp32 number to its quotient.  The scale's divisor is a constant, so one step on
+// the remainder does (P. W. Markstein, IBM J. Res. Dev. 34, 1990): with q = c times
+// the rounded 1 / fmax, the remainder c - fmax q is exact and q + (c - fmax q) / fmax
+// rounds to c / fmax.  All 1.9e9 fp32 numbers c from 2^-100 to infinity were compared
+// with the division, for both types; q alone is another number for 55 % of them.
 template <int FMT>
 __device__ __forceinline__ float fp8_scale(float amax) {
-  return fmaxf(amax, kFp8Tiny) * (1.0f / fp8_max<FMT>());
+  constexpr float kInv = 1.0f / fp8_max<FMT>();
+  const float c = fmaxf(amax, kFp8Tiny), q = __fmul_rn(c, kInv);
+  const float s = __fmaf_rn(__fmaf_rn(-fp8_max<FMT>(), q, c), kInv, q);
+  return c <= 3.4028234663852886e38f ? s : q;  // infinity stays
 }
 template <int FMT>
 __device__ __forceinline__ float fp8_factor(float amax) {

@@ -96,6 +96,53 @@ def test_quant_extremes(cuda_lib, fmt):
     assert (got[1, :128] == {"e4m3": 0.0, "e5m2": 0.0546875}[fmt]).all()
 
 
+def _quotients(amax, fmt="e4m3"):
+    """The fp32 scales of blocks whose largest magnitudes (fp32 values) are amax: correctly rounded quotients."""
+    amax = np.maximum(np.asarray(amax, np.float32), np.float32(O.TINY))
+    return amax / np.float32(O.FMAX[fmt])
+
+
+def _same32(got, want):
+    got = got.cpu().numpy()
+    assert got.shape == want.shape and got.dtype == want.dtype == np.float32
+    bad = got.view(np.uint32) != want.view(np.uint32)
+    assert not bad.any(), f"{bad.sum()}/{bad.size} scales are not the nearest fp32 number"
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_scales_are_correctly_rounded_quotients(cuda_lib, fmt):
+    """S = c / fmax to the last bit, wherever c is known to the last bit."""
+    B, f = cuda_lib, TYPES[fmt]
+    x = _bf(300, 1040, seed=1, scale=0.3)
+    x[7] *= 1e30
+    x[8] *= 1e-30
+    x[9] = 0.0
+    amax = lambda form: O.block_max(num(x), form)
+    o = B.quant_fp8(x.cuda(), cols=True, fmt=f)
+    _same32(o["Sr"], _quotients(amax("rows"), fmt))
+    _same32(o["Sc"], _quotients(amax("cols"), fmt))
+    _same32(B.quant_fp8_blocks(x.cuda(), fmt=f)["S"], _quotients(amax("blocks"), fmt))
+    two = torch.full((300,), 2.0)   # scaled by a power of two: c is exact
+    o = B.quant_fp8(x.cuda(), cols=True, rowvec=two.cuda(), fmt=f)
+    _same32(o["Sr"], _quotients(2 * amax("rows"), fmt))
+    _same32(o["Sc"], _quotients(2 * amax("cols"), fmt))
+
+
+def test_scales_of_the_norm_and_of_the_checkpoint_are_correctly_rounded(cuda_lib):
+    B = cuda_lib
+    x, g = _bf(40, 1040, seed=2).cuda(), (1 + 0.1 * _randn(1040, seed=3)).bfloat16().cuda()
+    o = B.rmsnorm_fp8_fwd(x, g, 1e-6)
+    n = x.float() * o["r"][:, None] * g.float()   # the kernel's own fp32 products
+    _same32(o["S"], _quotients(O.block_max(num(n), "rows")))
+    for M in (5, 100):  # few rows, and tiles: sums of small integers are exact
+        rng = np.random.default_rng(M)
+        a, w = rng.integers(-8, 9, (M, 128)), rng.integers(-8, 9, (512, 128))
+        e4 = lambda v: torch.from_numpy(v).float().to(TYPES["e4m3"]).cuda()
+        one = lambda *s: torch.ones(*s, device="cuda")
+        o = B.gemm_swiglu_fp8(e4(a), one(1, M), e4(w), one(4, 1))
+        _same32(o["SAB"], _quotients(O.block_max(a @ w.T, "rows")))
+
+
 # ------------------------------------------------------------------ GEMM
 
 def _gemm_case(B, M, N, K, a_mn, b_mn, blocks, fa, fb, f32, seed=0):
