@@ -664,7 +664,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
 #pragma unroll 1
       for (int left = num_kb; left > 0; left -= F8_GROUP, ++groups) {
         mbar_wait_drain(smem_u32(&sfull[groups & 1]), (groups >> 1) & 1u, wctl, (2 + q) << 8 | kWaitFull);
-        if (*abort_flag) break;
+        // A vote: the lanes come out of the wait one by one while another warp may
+        // be setting the flag, and what follows needs the whole warp.
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
         const float* sc = sScale + (groups & 1) * GROUP_FLOATS;
         const float* cs = sc + F8_GROUP * 128 + (VEC ? h * 128 + lane % 4 * 2 : EPI == F8_EPI_SWIGLU ? 0 : h);
         sc += q * 32 + (VEC ? lane / 4 : lane);

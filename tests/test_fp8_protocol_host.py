@@ -1,0 +1,24 @@
+"""Rules that the 8-bit GEMM's source keeps so that its waits end (CPU only).
+
+What these guard against would hang a GPU, so it is checked by reading.
+"""
+
+import os
+import re
+
+from gemm_epilogue_fusion_tmem_b200 import build
+
+SRC = open(os.path.join(build.CSRC, "coda_gemm_fp8.cuh")).read()
+
+
+def _drain():
+    """The drain warps' part of the tile kernel: from its heading to the set-down of the CTA."""
+    return SRC[SRC.index("drain and epilogue (both CTAs)"):SRC.index("few rows\n")]
+
+
+def test_a_drain_warp_leaves_its_loops_as_a_whole():
+    """tcgen05.ld.sync.aligned and __syncwarp need every lane: a lane that saw the abort flag
+    while another did not would leave that one waiting for good."""
+    left = [line.strip() for line in _drain().splitlines() if "abort_flag" in line and re.search(r"\b(break|return)\b", line)]
+    assert len(left) >= 3
+    assert all("__any_sync(0xffffffffu, *abort_flag)" in line for line in left), left
