@@ -58,6 +58,7 @@ def library() -> ctypes.CDLL:
             "coda_status_query": (I, [P, P, ctypes.POINTER(ctypes.c_uint32)]),
             "coda_set_wait_limit_ns": (None, [ctypes.c_uint64]),
             "coda_selftest_wait_timeout": (I, [P, ctypes.c_uint64, P]),
+            "coda_selftest_fp8_silence": (I, [I, I]),
             "coda_profile_arm": (I, [I, P, P]),
             "coda_gemm_workspace_bytes": (S, []),
             "coda_gemm": (I, [P, P, P, I, I, I, I, I, P, S, P]),
@@ -114,7 +115,7 @@ def library() -> ctypes.CDLL:
 
 # Host-side entry points that enqueue no GPU work get no NVTX range.
 _UNRANGED = {"coda_status_string", "coda_version", "coda_set_wait_limit_ns", "coda_profile_arm",
-             "coda_status_query", "coda_static_status_query"}
+             "coda_status_query", "coda_static_status_query", "coda_selftest_fp8_silence"}
 
 
 class _Ranged:
@@ -247,6 +248,15 @@ def profile_arm(kernel: int, start=None, stop=None) -> None:
 def selftest_wait_timeout(ws: Workspace, limit_ns: int) -> None:
     """Launch the bounded-wait self-test (a wait that must time out) on the current stream."""
     _check(library().coda_selftest_wait_timeout(ws.ptr(), int(limit_ns), _stream()), "coda_selftest_wait_timeout")
+
+
+FP8_ROLE_LOADS, FP8_ROLE_MMA, FP8_ROLE_SCALES = 1, 2, 3
+
+
+def selftest_fp8_silence(role: int, cta: int = 0) -> None:
+    """Keep one role of block `cta` silent in this thread's next 8-bit product, so that its waits run out
+    (role 0 disarms); see coda_selftest_fp8_silence."""
+    _check(library().coda_selftest_fp8_silence(int(role), int(cta)), "coda_selftest_fp8_silence")
 
 
 # ------------------------------------------------------------------ entry points

@@ -9,6 +9,9 @@
 namespace coda {
 namespace {
 
+// Armed by coda_selftest_fp8_silence for this thread's next 8-bit product.
+thread_local uint32_t g_fp8_silent = 0;
+
 constexpr int kScaleBlock = 128;  // values per scale along a blocked axis
 constexpr int kMax8Cols = 1 << 22;  // columns of the light passes' matrices: 32-bit offsets in a 128-row tile
 
@@ -88,6 +91,7 @@ coda_status launch_gemm8(const CUtensorMap& ta, const CUtensorMap& tb, Gemm8Para
   int clusters = 0;
   CODA_TRY((gemm8_clusters<EPI, A_MN, B_MN, VEC, SPLIT>(parts, clusters)));
   p.wait_limit_ns = g_wait_limit_ns.load();
+  p.silent = std::exchange(g_fp8_silent, 0u);
   p.kernel_id = 0x40 + (uint32_t)(EPI * 8 + (A_MN ? 4 : 0) + (B_MN ? 2 : 0) + (VEC ? 1 : 0)) + (SPLIT ? 0x40 : 0);
   const long long tiles = (long long)p.num_m_tiles * p.num_n_tiles;
   const int units = SPLIT ? (int)tiles : (int)std::min<long long>(tiles, clusters);
@@ -212,6 +216,12 @@ coda_status rms8_bwd(const RmsBwdParams& p, void* stream) {
 }  // namespace coda
 
 extern "C" {
+
+coda_status coda_selftest_fp8_silence(int role, int cta) {
+  if (role < 0 || role > CODA_FP8_ROLE_SCALES || cta < 0 || cta >= 1 << 20) return CODA_ERR_INVALID_ARG;
+  g_fp8_silent = role == 0 ? 0u : (uint32_t)cta << 2 | (uint32_t)role;
+  return CODA_OK;
+}
 
 // ------------------------------------------------------------------ quantiser
 

@@ -86,7 +86,11 @@ struct Gemm8Params {
   uint32_t* status;
   unsigned long long wait_limit_ns;
   uint32_t kernel_id;
+  uint32_t silent;  // self-test: a role that does nothing (f8_silent), 0 for none
 };
+
+// True in the CTA and role that a self-test keeps silent, so that the waits on it run out.
+__device__ __forceinline__ bool f8_silent(uint32_t silent, uint32_t role) { return silent == (blockIdx.x << 2 | role); }
 
 // Instruction descriptor for kind::f8f6f4, fp32 D (bit positions as make_idesc_bf16;
 // operand formats 0 = e4m3, 1 = e5m2, which may differ between A and B).
@@ -189,7 +193,8 @@ struct DrainCtl {
 // drain is latency-bound, so success costs a poll and a branch: there is no
 // result.  A wait that runs out, or sees that another role has given up, sets or
 // leaves the abort flag and returns; the caller looks at the flag every few
-// blocks and what it computed since then is not stored.
+// blocks and what its CTA computed since then is not stored.  (The other CTA of
+// the pair comes to the same end: no MMA is issued after a wait that gave up.)
 __device__ __forceinline__ void mbar_wait_drain(uint32_t bar, uint32_t parity, uint32_t ctl, uint32_t detail) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .u32 f;\n\t.reg .u64 t0, t1, lim;\n\t"
@@ -202,6 +207,26 @@ __device__ __forceinline__ void mbar_wait_drain(uint32_t bar, uint32_t parity, u
       "DONE:\n\t}\n" ::"r"(bar),
       "r"(parity), "r"(ctl), "r"(detail)
       : "memory");
+}
+// The same for the thread that issues the MMAs.  It may not go on after a wait that
+// gave up (false): the operands may not have landed, the buffer may not have been
+// drained, and its commit would tell both CTAs that a product is complete.
+__device__ __forceinline__ bool mbar_wait_issue(uint32_t bar, uint32_t parity, uint32_t ctl, uint32_t detail) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .u32 f;\n\t.reg .u64 t0, t1, lim;\n\tmov.u32 %0, 1;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+      "mov.u64 t0, %%globaltimer;\n\tld.shared.u64 lim, [%3 + 8];\n"
+      "POLL:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+      "ld.volatile.shared.u32 f, [%3];\n\tsetp.ne.u32 p, f, 0;\n\t@p bra GAVE_UP;\n\t"
+      "mov.u64 t1, %%globaltimer;\n\tsub.u64 t1, t1, t0;\n\tsetp.lt.u64 p, t1, lim;\n\t@p bra POLL;\n\t"
+      "st.volatile.shared.u32 [%3], %4;\n"
+      "GAVE_UP:\n\tmov.u32 %0, 0;\n"
+      "DONE:\n\t}\n"
+      : "=&r"(ok)
+      : "r"(bar), "r"(parity), "r"(ctl), "r"(detail)
+      : "memory");
+  return ok != 0;
 }
 // Wait for copies or MMAs of this CTA's own, whether or not a role has given up:
 // they must not be in flight when their shared memory or TMEM is released.
@@ -512,7 +537,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       const uint64_t hint = l2_policy_evict_normal();
       int stage = 0;
       uint32_t phase = 0;
-      bool ok = true;
+      bool ok = !f8_silent(p.silent, CODA_FP8_ROLE_LOADS);
       for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
         int m_blk, n_blk;
         tile_coords(tile, p.num_m_tiles, p.num_n_tiles, p.group_m, m_blk, n_blk);
@@ -557,12 +582,14 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       const uint64_t a_desc0 = make_sdesc_sw128(smem_u32(sA), 16, 1024);
       const uint64_t b_desc0 = (B_MN ? make_sdesc_sw64(smem_u32(sB), 16, 512) : make_sdesc_sw128(smem_u32(sB), 16, 1024)) +
                                half * (8192 >> 4);
-      for (int tile = first_tile; tile < num_tiles; tile += tile_step) {
+      bool ok = !f8_silent(p.silent, CODA_FP8_ROLE_MMA);
+      for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
 #pragma unroll 1
         for (int kb = num_kb; kb > 0; --kb, ++it) {
           const uint32_t buf = (it & 1) * 2 + half;
-          mbar_wait_drain(full_s + stage * 8, phase, wctl, 1 << 8 | kWaitFull);
-          mbar_wait_drain(smem_u32(tempty) + buf * 8, ((it >> 1) & 1u) ^ 1u, wctl, 1 << 8 | kWaitAccEmpty);
+          ok = mbar_wait_issue(full_s + stage * 8, phase, wctl, 1 << 8 | kWaitFull) &&
+               mbar_wait_issue(smem_u32(tempty) + buf * 8, ((it >> 1) & 1u) ^ 1u, wctl, 1 << 8 | kWaitAccEmpty);
+          if (!ok) break;
           tc_fence_after();
           // K-major: 32 bytes inside the 128-byte swizzled row; MN-major: 32 k
           // rows of 128 bytes (A) or 64 bytes (B, one 64-row half per CTA).
@@ -578,7 +605,6 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             phase ^= 1u;
           }
         }
-        if (*abort_flag) break;
       }
       umma_commit_pair(mapa_shared(smem_u32(mma_done), leader));
       mbar_wait_own(mma_done, 0, ctl.limit_ns);
@@ -586,7 +612,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       // ---------------------------------------------------------------- scales (both CTAs)
       int st = 0;
       uint32_t phase = 0;
-      bool ok = true;
+      bool ok = !f8_silent(p.silent, CODA_FP8_ROLE_SCALES);
       for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
         int m_blk, n_blk;
         tile_coords(tile, p.num_m_tiles, p.num_n_tiles, p.group_m, m_blk, n_blk);

@@ -96,6 +96,18 @@ void coda_set_wait_limit_ns(uint64_t ns);
  * it with coda_status_clear. */
 coda_status coda_selftest_wait_timeout(void* ws, uint64_t limit_ns, void* stream);
 
+/* Self-test of the 8-bit products' failure path (coda_gemm_fp8,
+ * coda_gemm_swiglu_fp8): in the next such product launched by the calling host
+ * thread, one role of block `cta` does nothing, so that the waits on it run out
+ * after the limit (coda_set_wait_limit_ns; give a short one, not below a
+ * millisecond) as they would on an arrival that was lost.  The product records
+ * CODA_ERR_DEVICE_TIMEOUT, stores nothing of the tile that was not completed and
+ * returns; the tiles of other blocks are as ever.  Role 0 disarms. */
+#define CODA_FP8_ROLE_LOADS 1  /* the copies of the operands */
+#define CODA_FP8_ROLE_MMA 2    /* the products (a pair's first block issues them) */
+#define CODA_FP8_ROLE_SCALES 3 /* the copies of the scales (tiles of 256 x 256) */
+coda_status coda_selftest_fp8_silence(int role, int cta);
+
 /* Kernel timing hook.  Arms a one-shot pair of CUDA events around the next
  * launch, from the calling host thread, of the kernel `kernel` names, whichever
  * entry point makes it: a GEMM by its epilogue (CODA_EPI_*) or a light pass

@@ -22,3 +22,12 @@ def test_a_drain_warp_leaves_its_loops_as_a_whole():
     left = [line.strip() for line in _drain().splitlines() if "abort_flag" in line and re.search(r"\b(break|return)\b", line)]
     assert len(left) >= 3
     assert all("__any_sync(0xffffffffu, *abort_flag)" in line for line in left), left
+
+
+def test_no_mma_is_issued_after_a_wait_that_gave_up():
+    """The operands may not have landed then, and the commit would tell the other CTA of the pair that a
+    product is complete: the issuer's waits have a result and it is looked at before anything else."""
+    part = SRC[SRC.index("MMA issuers (pair's leader)"):SRC.index("// ---------------------------------------------------------------- scales")]
+    waits, mma = part.index("mbar_wait_issue"), part.index("umma_f8_stage_pair<")
+    assert "mbar_wait_drain" not in part and part.count("mbar_wait_issue") == 2
+    assert "if (!ok) break;" in part[waits:mma]

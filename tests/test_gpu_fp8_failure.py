@@ -1,0 +1,111 @@
+"""The 8-bit products when an arrival is lost: every wait ends, the status word says so, nothing is
+stored of the tile that was not completed, and the next call is as ever.
+
+One role of one block is kept silent (coda_selftest_fp8_silence), so that the waits on it run out.  The
+limit is far longer than any copy or product takes, so nothing is in flight when a role gives up.
+"""
+
+import contextlib
+import time
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+TIMEOUT = 7
+LIMIT_NS = 50_000_000
+LOADS, MMA, SCALES = 1, 2, 3
+
+
+@contextlib.contextmanager
+def silence(B, role, cta):
+    B.set_wait_limit_ns(LIMIT_NS)
+    B.selftest_fp8_silence(role, cta)
+    try:
+        yield
+    finally:
+        B.selftest_fp8_silence(0)
+        B.set_wait_limit_ns(4_000_000_000)
+
+
+def _bf(*shape, seed):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
+
+
+def _raw(t):
+    return t.view(torch.uint8) if t.element_size() == 1 else t
+
+
+def _call(B, name, M=600, N=512, K=1280):
+    """(function of (out, ws) that runs the product on fixed operands, its outputs as they are before)."""
+    if name == "wgrad":
+        a, b = (B.quant_fp8(_bf(K, n, seed=n), rows=False, cols=True) for n in (M + 8, N))
+        args = (a["Qc"], a["Sc"], b["Qc"], b["Sc"], M + 8, N, K)
+        kw = dict(a_mn_major=True, b_mn_major=True, b_blocks=False, out_dtype=torch.float32, accumulate=True)
+        return (lambda out, ws: B.gemm_fp8(*args, **kw, out=out["C"], ws=ws)), {"C": torch.full((M + 8, N), 7.0, device="cuda")}
+    x = B.quant_fp8(_bf(M, K, seed=1))
+    if name == "swiglu":
+        w = B.quant_fp8_blocks(_bf(2 * N, K, seed=2))
+        new = {k: torch.full(s, 1.5, device="cuda").to(torch.float8_e4m3fn) for k, s in (("Y", (M, N)), ("AB", (M, 2 * N)))}
+        new |= {k: torch.full(s, 7.0, device="cuda") for k, s in (("SY", (N // 128, M)), ("SAB", (N // 64, M)))}
+        return (lambda out, ws: B.gemm_swiglu_fp8(x["Qr"], x["Sr"], w["Q"], w["S"], out=out, ws=ws)), new
+    w = B.quant_fp8_blocks(_bf(N, K, seed=2))
+    f32 = name == "add"
+    new = torch.full((M, N), 7.0, device="cuda", dtype=torch.float32 if f32 else torch.bfloat16)
+    kw = dict(out_dtype=new.dtype, accumulate=f32)
+    return (lambda out, ws: B.gemm_fp8(x["Qr"], x["Sr"], w["Q"], w["S"], M, N, K, **kw, out=out["C"], ws=ws)), {"C": new}
+
+
+def _run(B, name, role, cta, tile, **sizes):
+    """Run once as ever and once with a silent role; returns for each output (before, as ever, silent) and the
+    part `tile` of it."""
+    call, new = _call(B, name, **sizes)
+    ws = B.Workspace(256)
+    clone = lambda d: {k: v.clone() for k, v in d.items()}
+    want = clone(new)
+    call(want, ws)
+    assert ws.query() == (0, 0)
+    got = clone(new)
+    t0 = time.perf_counter()
+    with silence(B, role, cta):
+        call(got, ws)
+        status, detail = ws.query()
+    assert time.perf_counter() - t0 < 3.0
+    assert status == TIMEOUT and detail >> 16 != 0
+    for k in new:
+        here = tile(k, new[k])
+        before, silent, ever = _raw(new[k]), _raw(got[k]), _raw(want[k])
+        assert torch.equal(silent[here], before[here]), f"{k}: the tile was stored"
+        rest = torch.ones(new[k].shape, dtype=torch.bool, device="cuda")
+        rest[here] = False
+        assert torch.equal(silent[rest], ever[rest]), f"{k}: other tiles"
+    ws.clear()
+    again = clone(new)
+    call(again, ws)
+    assert ws.query() == (0, 0)
+    for k in new:
+        assert torch.equal(_raw(again[k]), _raw(want[k])), k
+
+
+def _first_tile(name):
+    """What block 0's pair computes: 256 rows, and 256 columns or the 128 of a gate/up tile."""
+    def part(key, t):
+        if name != "swiglu":
+            return (slice(0, 256), slice(0, 256))
+        if key in ("SY", "SAB"):
+            blocks = t.shape[0]
+            rows = [0] if key == "SY" else [0, blocks // 2]
+            return (torch.tensor(rows, device="cuda")[:, None], torch.arange(256, device="cuda")[None, :])
+        cols = torch.arange(128, device="cuda")
+        if key == "AB":
+            cols = torch.cat([cols, cols + t.shape[1] // 2])
+        return (torch.arange(256, device="cuda")[:, None], cols[None, :])
+    return part
+
+
+@pytest.mark.parametrize("name", ["bf16", "add", "wgrad", "swiglu"])
+@pytest.mark.parametrize("role,cta", [(SCALES, 0), (SCALES, 1), (MMA, 0)])
+def test_tile_of_a_pair_that_gave_up_is_not_stored(cuda_lib, name, role, cta):
+    """The scales of either CTA, or the products: neither CTA of the pair stores its rows of the tile."""
+    _run(cuda_lib, name, role, cta, _first_tile(name))
