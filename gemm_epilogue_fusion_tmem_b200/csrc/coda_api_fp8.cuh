@@ -154,6 +154,7 @@ coda_status launch_skinny8(const CUtensorMap& tw, const CUtensorMap& tx, Skinny8
   while (splits < 8 && tiles * splits * 2 <= 2 * g_dev[dev].num_sms && splits * 4 <= p.k_blocks) splits *= 2;
   p.idesc = (p.idesc & ~(0x3Fu << 17)) | ((uint32_t)(TN >> 3) << 17);
   p.wait_limit_ns = g_wait_limit_ns.load();
+  p.silent = std::exchange(g_fp8_silent, 0u);
   p.kernel_id = 0x60 + (uint32_t)(TN / 16 * 2 + (SWIGLU ? 1 : 0));
   g_launch_tag = SWIGLU ? CODA_KERNEL_GEMM_SWIGLU_FP8 : CODA_KERNEL_GEMM_FP8;
   const cudaError_t e =

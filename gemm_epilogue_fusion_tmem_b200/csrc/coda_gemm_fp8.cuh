@@ -375,6 +375,24 @@ __device__ __forceinline__ void f8_store_row64(uint8_t* dst, bool wide, Value va
   }
 }
 
+// Record a wait of a drain warp or an MMA issuer that ran out (mbar_wait records its own and sets 1).
+__device__ __forceinline__ void f8_record(uint32_t flag, uint32_t* status, uint32_t kernel_id) {
+  if (flag <= 1 || status == nullptr) return;
+  atomicCAS(status, 0u, 7u /* CODA_ERR_DEVICE_TIMEOUT */);
+  atomicCAS(status + 1, 0u, (kernel_id << 16) | flag);
+}
+// Where the CTAs of a cluster add each other's partial tiles: if a role of this CTA
+// gave up, its partial tile is not one, and every CTA of the cluster has to know
+// before the barrier behind which it reads it.  By one thread, when all the CTA's
+// roles have come to their end; costs a look at the flag when none gave up.
+__device__ __forceinline__ void f8_tell_cluster(uint32_t* abort_flag, int ctas, uint32_t* status, uint32_t kernel_id) {
+  const uint32_t flag = *const_cast<volatile uint32_t*>(abort_flag);
+  if (flag == 0) return;
+  f8_record(flag, status, kernel_id);
+  for (int r = 0; r < ctas; ++r)
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(abort_flag), (uint32_t)r)), "r"(1u) : "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_nctarank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
@@ -662,6 +680,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     if constexpr (SPLIT) {
       __syncwarp();
       cluster_sync();
+      // Every role of the cluster has come to its end.  By a warp that is known uniform:
+      // behind threadIdx.x == 0 the whole kernel took longer (1001 x 2048 x 16384 45 us for 36).
+      if (warp == 2 && lane == 0) f8_tell_cluster(&drain_ctl->abort, (int)cluster_nctarank(), p.status, p.kernel_id);
       cluster_sync();
     }
   } else {
@@ -847,7 +868,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     }
     if constexpr (SPLIT) {
       if (!given) cluster_sync();
-      cluster_sync();  // all partial tiles are there
+      cluster_sync();  // all partial tiles are there, or the abort flag is set in every CTA
       if (!*abort_flag) f8_finish_share<EPI>(p, smem);
     }
   }
@@ -855,10 +876,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   tc_fence_before();
   cluster_sync();
   if (*abort_flag) {
-    if (threadIdx.x == 0 && *abort_flag != 1 && p.status != nullptr) {  // a drain warp's wait
-      atomicCAS(p.status, 0u, 7u /* CODA_ERR_DEVICE_TIMEOUT */);
-      atomicCAS(p.status + 1, 0u, (p.kernel_id << 16) | (uint32_t)*abort_flag);
-    }
+    if (threadIdx.x == 0) f8_record((uint32_t)*abort_flag, p.status, p.kernel_id);
     // A role gave up: let the last (up to STAGES) copies land before shared
     // memory is released.  Every wait here is bounded too.
     if (warp == 0 && lane == 0 && rank == 0) {
@@ -920,6 +938,7 @@ struct Skinny8Params {
   uint32_t* status;
   unsigned long long wait_limit_ns;
   uint32_t kernel_id;
+  uint32_t silent;  // as Gemm8Params
 };
 
 __device__ __forceinline__ void umma_f8_stage(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
@@ -1023,7 +1042,7 @@ __global__ void __launch_bounds__(F8S_THREADS, 2)
       int stage = 0;
       uint32_t phase = 0;
       int issued = 0;
-      for (; issued < nkb; ++issued) {
+      for (const int n = f8_silent(p.silent, CODA_FP8_ROLE_LOADS) ? 0 : nkb; issued < n; ++issued) {
         if (!mbar_wait(&empty[stage], phase ^ 1u, ctl, 0, kWaitEmpty)) break;
         uint8_t* dst = smem + stage * C::STAGE_BYTES;
         const int k0 = (kb0 + issued) * F8_BK;
@@ -1045,7 +1064,7 @@ __global__ void __launch_bounds__(F8S_THREADS, 2)
       int stage = 0;
       uint32_t phase = 0;
       const uint64_t desc0 = make_sdesc_sw128(smem_u32(smem), 16, 1024);
-      for (int kb = 0; kb < nkb; ++kb) {
+      for (int kb = f8_silent(p.silent, CODA_FP8_ROLE_MMA) ? nkb : 0; kb < nkb; ++kb) {
         if (!mbar_wait(&full[stage], phase, ctl, 1, kWaitFull)) break;
         const int buf = kb % C::BUFS;
         if (!mbar_wait(&tempty[buf], ((uint32_t)(kb / C::BUFS) & 1u) ^ 1u, ctl, 1, kWaitAccEmpty)) break;
@@ -1150,7 +1169,10 @@ __global__ void __launch_bounds__(F8S_THREADS, 2)
 #pragma unroll
       for (int t = 0; t < TN; ++t) part[(w * TN + t) * 128 + row] = acc[w][t];
   }
-  if (splits > 1) cluster_sync();
+  if (splits > 1) {
+    if (threadIdx.x == 0) f8_tell_cluster(&drain_ctl->abort, splits, p.status, p.kernel_id);
+    cluster_sync();
+  }
   // This CTA's share of the tile's rows of A: [t0, t0 + share).
   const int share = TN / splits, t0 = rank * share;
   const int used = min(share, p.M - t0);  // rows that exist
@@ -1223,10 +1245,7 @@ __global__ void __launch_bounds__(F8S_THREADS, 2)
     }
   }
   if (splits > 1) cluster_sync();  // peers are done with this CTA's partial tile
-  if (threadIdx.x == 0 && *abort_flag > 1 && p.status != nullptr) {  // a drain warp's wait
-    atomicCAS(p.status, 0u, 7u /* CODA_ERR_DEVICE_TIMEOUT */);
-    atomicCAS(p.status + 1, 0u, (p.kernel_id << 16) | (uint32_t)*abort_flag);
-  }
+  if (threadIdx.x == 0) f8_record((uint32_t)*abort_flag, p.status, p.kernel_id);
   if (warp == 1) tmem_dealloc(tmem_base, C::TMEM);
 }
 

@@ -109,3 +109,31 @@ def _first_tile(name):
 def test_tile_of_a_pair_that_gave_up_is_not_stored(cuda_lib, name, role, cta):
     """The scales of either CTA, or the products: neither CTA of the pair stores its rows of the tile."""
     _run(cuda_lib, name, role, cta, _first_tile(name))
+
+
+def _few_rows_tile(name):
+    """The 128 columns that cluster 0 computes of a product of few rows."""
+    def part(key, t):
+        if key in ("SY", "SAB"):
+            rows = [0] if key == "SY" else [0, t.shape[0] // 2]
+            return (torch.tensor(rows, device="cuda")[:, None], torch.arange(t.shape[1], device="cuda")[None, :])
+        cols = torch.arange(128, device="cuda")
+        if key == "AB":
+            cols = torch.cat([cols, cols + t.shape[1] // 2])
+        return (torch.arange(t.shape[0], device="cuda")[:, None], cols[None, :])
+    return part
+
+
+@pytest.mark.parametrize("name", ["bf16", "add"])
+@pytest.mark.parametrize("role,cta", [(MMA, 2), (MMA, 0), (SCALES, 7), (SCALES, 2)])
+def test_shared_tile_of_which_a_part_is_missing_is_not_stored(cuda_lib, name, role, cta):
+    """Four pairs share the reduction of a tile and one of them gives up: none adds what is left in its place."""
+    _run(cuda_lib, name, role, cta, _first_tile(name), M=300, K=4112)
+
+
+@pytest.mark.parametrize("name", ["bf16", "add", "swiglu"])
+@pytest.mark.parametrize("M,K,role,cta", [(5, 4096, MMA, 3), (5, 4096, LOADS, 0), (20, 2048, MMA, 7), (32, 2048, LOADS, 5),
+                                          (3, 256, MMA, 0)])
+def test_few_rows_of_which_a_part_is_missing_are_not_stored(cuda_lib, name, M, K, role, cta):
+    """The same for the CTAs that share the reduction of a product of few rows."""
+    _run(cuda_lib, name, role, cta, _few_rows_tile(name), M=M, N=256, K=K)
