@@ -182,10 +182,10 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 
 // Control words of the drain's waits, in shared memory: the abort flag (nonzero:
 // some role gave up; the detail word's role and reason, or 1 when mbar_wait has
-// recorded it) and the limit.
+// recorded it) and the limit; and, at the end, the stages this CTA's producer issued.
 struct DrainCtl {
   uint32_t abort;
-  uint32_t unused;
+  uint32_t issued;
   uint64_t limit_ns;
 };
 
@@ -227,13 +227,6 @@ __device__ __forceinline__ bool mbar_wait_issue(uint32_t bar, uint32_t parity, u
       : "r"(bar), "r"(parity), "r"(ctl), "r"(detail)
       : "memory");
   return ok != 0;
-}
-// Wait for copies or MMAs of this CTA's own, whether or not a role has given up:
-// they must not be in flight when their shared memory or TMEM is released.
-__device__ __forceinline__ void mbar_wait_own(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < limit_ns) {
-  }
 }
 // Arrive where `pred` is set, without a branch.
 __device__ __forceinline__ void mbar_arrive_if(uint32_t bar, uint32_t pred) {
@@ -625,7 +618,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         }
       }
       umma_commit_pair(mapa_shared(smem_u32(mma_done), leader));
-      mbar_wait_own(mma_done, 0, ctl.limit_ns);
+      mbar_wait_own(mma_done, 0, ctl, 1);
     } else if (warp == 2) {
       // ---------------------------------------------------------------- scales (both CTAs)
       int st = 0;
@@ -873,16 +866,17 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     }
   }
 
+  if (warp == 0 && lane == 0) drain_ctl->issued = (uint32_t)issued;
   tc_fence_before();
   cluster_sync();
   if (*abort_flag) {
     if (threadIdx.x == 0) f8_record((uint32_t)*abort_flag, p.status, p.kernel_id);
-    // A role gave up: let the last (up to STAGES) copies land before shared
-    // memory is released.  Every wait here is bounded too.
-    if (warp == 0 && lane == 0 && rank == 0) {
-      const int first = issued > S ? issued - S : 0;
-      for (int i = first; i < issued; ++i) mbar_wait_own(&full[i % S], (uint32_t)((i / S) & 1), ctl.limit_ns);
-    }
+    // A role gave up: the last (up to STAGES) copies of both CTAs land before
+    // shared memory is released.  Copies are only left over where the leader's
+    // issuers stopped, so the leader's flag is set.
+    if (warp == 0 && lane == 0 && rank == 0)
+      pair_copies_landed<S>(full, issued, (int)ld_cluster_u32(mapa_shared(smem_u32(&drain_ctl->issued), leader + 1)),
+                            F8_STAGE_BYTES, ctl);
     __syncthreads();
   }
   cluster_sync();
@@ -1057,7 +1051,7 @@ __global__ void __launch_bounds__(F8S_THREADS, 2)
       }
       // Every copy has landed before this CTA's shared memory is used for anything else or released.
       for (int i = issued > S ? issued - S : 0; i < issued; ++i)
-        mbar_wait_own(&full[i % S], (uint32_t)((i / S) & 1), ctl.limit_ns);
+        mbar_wait_own(&full[i % S], (uint32_t)((i / S) & 1), ctl, 0);
     }
   } else if (warp == 1) {
     if (elect_one()) {
@@ -1082,7 +1076,7 @@ __global__ void __launch_bounds__(F8S_THREADS, 2)
         }
       }
       umma_commit(mma_done);
-      mbar_wait_own(mma_done, 0, ctl.limit_ns);
+      mbar_wait_own(mma_done, 0, ctl, 1);
     }
   } else {
     const int q = warp & 3;

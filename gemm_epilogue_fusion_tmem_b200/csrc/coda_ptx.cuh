@@ -104,6 +104,22 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   }
 }
 
+// Wait for copies or MMAs of this CTA's own, whether or not a role has given up:
+// they must not be in flight when their shared memory or TMEM is released.  What
+// was issued does complete, in microseconds, so the bound is not the configurable
+// limit, which may be shorter than that, but at least two seconds; running out
+// even then is recorded.
+constexpr uint64_t kOwnWaitNs = 2000000000ull;
+__device__ __forceinline__ void mbar_wait_own(uint64_t* bar, uint32_t parity, const WaitCtl& c, uint32_t role) {
+  const uint64_t t0 = global_timer_ns(), limit = c.limit_ns > kOwnWaitNs ? c.limit_ns : kOwnWaitNs;
+  while (!mbar_try_wait(bar, parity)) {
+    if (global_timer_ns() - t0 > limit) {
+      record_timeout(c, role, kWaitDrain);
+      return;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {
@@ -303,6 +319,34 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t saddr, uint32_t rank) {
 // Arrive on an mbarrier given by its shared::cluster address (own CTA or the peer).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+// Take `bytes` off what the barrier's phase still expects: copies that were announced and will not come.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+// After a role of a pair gave up: wait until the last copies of both CTAs have landed.
+// The leader's full barriers count the bytes of both, `bytes` each, and the two may
+// have stopped at different stages (mine, theirs: stages issued by the leader and by
+// the other CTA; at most STAGES apart, since both wait for the same hand-backs).  A
+// stage that only the other issued is announced here; the half of one that it did not
+// issue is taken off again.  By one thread of the leader, when all roles of the pair
+// have come to their end.
+template <int STAGES>
+__device__ __forceinline__ void pair_copies_landed(uint64_t* full, int mine, int theirs, uint32_t bytes, const WaitCtl& c) {
+  const int end = mine > theirs ? mine : theirs;
+  for (int i = end > STAGES ? end - STAGES : 0; i < end; ++i) {
+    uint64_t* bar = &full[i % STAGES];
+    if (i >= mine) mbar_arrive_expect_tx(bar, bytes);
+    else if (i >= theirs) mbar_complete_tx(bar, bytes);
+    mbar_wait_own(bar, (uint32_t)((i / STAGES) & 1), c, 0);
+  }
 }
 
 // Tile load of one CTA of a pair whose completion bytes go to the mbarrier at

@@ -31,3 +31,18 @@ def test_no_mma_is_issued_after_a_wait_that_gave_up():
     waits, mma = part.index("mbar_wait_issue"), part.index("umma_f8_stage_pair<")
     assert "mbar_wait_drain" not in part and part.count("mbar_wait_issue") == 2
     assert "if (!ok) break;" in part[waits:mma]
+
+
+def test_waits_for_own_copies_do_not_end_with_the_configurable_limit():
+    """coda_set_wait_limit_ns may be as short as a microsecond, less than a copy takes: the waits before shared
+    memory or TMEM is released have a bound of their own, and running out of it is recorded."""
+    ptx = open(os.path.join(build.CSRC, "coda_ptx.cuh")).read()
+    own = ptx[ptx.index("void mbar_wait_own("):]
+    own = own[:own.index("\n}\n")]
+    assert "c.limit_ns > kOwnWaitNs ? c.limit_ns : kOwnWaitNs" in own and "record_timeout(c, role, kWaitDrain)" in own
+    assert int(re.search(r"kOwnWaitNs = (\d+)ull", ptx)[1]) >= 10**9
+    waits = re.findall(r"mbar_wait_own\(.*?\);", SRC)
+    assert len(waits) >= 3 and all(", ctl, " in w for w in waits)
+    # Every commit that tells that all MMAs are complete is waited for before the roles meet.
+    for m in re.finditer(r"umma_commit(_pair)?\([^;]*mma_done[^;]*;\s*(\w+)\(", SRC):
+        assert m[2] == "mbar_wait_own"

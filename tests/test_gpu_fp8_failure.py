@@ -111,6 +111,14 @@ def test_tile_of_a_pair_that_gave_up_is_not_stored(cuda_lib, name, role, cta):
     _run(cuda_lib, name, role, cta, _first_tile(name))
 
 
+@pytest.mark.parametrize("name", ["bf16", "wgrad", "swiglu"])
+@pytest.mark.parametrize("cta", [0, 1])
+def test_copies_of_one_cta_of_a_pair_are_waited_for(cuda_lib, name, cta):
+    """One CTA's operand copies never start: the other's stages, announced or not, are settled before the
+    CTAs end, without waiting for bytes that will not come (six stages of at least two seconds each)."""
+    _run(cuda_lib, name, LOADS, cta, _first_tile(name), K=1920)
+
+
 def _few_rows_tile(name):
     """The 128 columns that cluster 0 computes of a product of few rows."""
     def part(key, t):
