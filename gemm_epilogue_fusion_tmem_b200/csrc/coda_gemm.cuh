@@ -556,6 +556,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint64_t* mma_done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* issued_slot = tmem_slot + 2;  // at the end: the stages this CTA's producer issued
 
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
@@ -727,7 +728,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // Every MMA issued by this thread has completed once mma_done fires.
       if constexpr (PAIR) umma_commit_pair(mapa_shared(smem_u32(mma_done), 0));
       else umma_commit(mma_done);
-      mbar_wait(mma_done, 0, ctl, 1, kWaitDrain);
+      mbar_wait_own(mma_done, 0, ctl, 1);
     }
   } else {
     // ---------------------------------------------------------------- epilogue (every CTA)
@@ -767,19 +768,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     es.finish();  // every tile store has completed before the CTA's shared memory is released
   }
 
+  if (warp == 0 && lane == 0) *issued_slot = (uint32_t)issued;
   tc_fence_before();
   if constexpr (PAIR) cluster_sync(); else __syncthreads();
   if (*abort_flag) {
-    // A role gave up: let the last (up to STAGES) copies land before shared
-    // memory is released.  Every wait here is bounded too.
+    // A role gave up: the last (up to STAGES) copies land before shared memory is
+    // released.  In a pair copies are only left over where the leader's issuer
+    // stopped, so the leader's flag is set.  Every wait here is bounded too.
     if (warp == 0 && lane == 0 && rank == 0) {
-      const int first = issued > S ? issued - S : 0;
-      for (int i = first; i < issued; ++i) {
-        const uint32_t par = (uint32_t)((i / S) & 1);
-        const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(&full[i % S], par) && global_timer_ns() - t0 < ctl.limit_ns) {
-        }
-      }
+      const int theirs = PAIR ? (int)ld_cluster_u32(mapa_shared(smem_u32(issued_slot), 1)) : issued;
+      pair_copies_landed<S>(full, issued, theirs, C::STAGE_BYTES, ctl);
     }
     __syncthreads();
   }

@@ -46,3 +46,11 @@ def test_waits_for_own_copies_do_not_end_with_the_configurable_limit():
     # Every commit that tells that all MMAs are complete is waited for before the roles meet.
     for m in re.finditer(r"umma_commit(_pair)?\([^;]*mma_done[^;]*;\s*(\w+)\(", SRC):
         assert m[2] == "mbar_wait_own"
+
+
+def test_the_bf16_gemm_waits_for_its_own_copies_and_mmas_too():
+    src = open(os.path.join(build.CSRC, "coda_gemm.cuh")).read()
+    after = src[src.index("else umma_commit(mma_done);"):]
+    assert after.splitlines()[1].strip().startswith("mbar_wait_own(mma_done, 0,")
+    end = src[src.index("es.finish();"):]
+    assert "pair_copies_landed<S>(" in end and "ctl.limit_ns" not in end
