@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import types
 
 import torch
 
@@ -56,6 +57,7 @@ def library() -> ctypes.CDLL:
             "coda_version": (I, []),
             "coda_status_clear": (I, [P, P]),
             "coda_status_query": (I, [P, P, ctypes.POINTER(ctypes.c_uint32)]),
+            "coda_shared_status": (I, [ctypes.POINTER(P)]),
             "coda_set_wait_limit_ns": (None, [ctypes.c_uint64]),
             "coda_selftest_wait_timeout": (I, [P, ctypes.c_uint64, P]),
             "coda_selftest_fp8_silence": (I, [I, I]),
@@ -115,7 +117,8 @@ def library() -> ctypes.CDLL:
 
 # Host-side entry points that enqueue no GPU work get no NVTX range.
 _UNRANGED = {"coda_status_string", "coda_version", "coda_set_wait_limit_ns", "coda_profile_arm",
-             "coda_status_query", "coda_static_status_query", "coda_selftest_fp8_silence"}
+             "coda_status_query", "coda_static_status_query", "coda_selftest_fp8_silence",
+             "coda_shared_status"}
 
 
 class _Ranged:
@@ -741,30 +744,35 @@ def _call(name: str, dev, *args) -> None:
             _check(getattr(_lib, name)(*args, torch._C._cuda_getCurrentRawStream(dev.index)), name)
 
 
-_status_ws: dict = {}   # by device index
-_graph_status: list = []  # words of calls captured before their device's first eager one
+class _SharedStatus(Workspace):
+    """The library's own status word of a device (coda_shared_status)."""
+
+    def __init__(self, dev):
+        ptr = _c_void_p()
+        with torch.cuda.device(dev):
+            _check(library().coda_shared_status(ctypes.byref(ptr)), "coda_shared_status")
+            word = {"shape": (256,), "typestr": "|u1", "data": (ptr.value, False), "version": 2}
+            self.buf = torch.as_tensor(types.SimpleNamespace(__cuda_array_interface__=word), device=dev)
+
+
+_status_ws: dict = {}   # by device index, from the first call outside a capture on
 
 
 def _status_workspace(dev) -> Workspace:
-    """The device's status word for calls that need no other scratch.  It is
-    never replaced, so captured graphs may keep its address.  A call that is
-    captured before the first eager one gets a word of its own, which lives as
-    long as the process: its graph may be replayed at any time."""
+    """The device's status word for calls that need no other scratch: the same
+    memory in every call, thread and captured graph, zero from the start."""
     ws = _status_ws.get(dev.index)
     if ws is None:
-        ws = Workspace(256, dev)
-        if torch.cuda.is_current_stream_capturing():
-            _graph_status.append(ws)
-        else:
-            torch.cuda.current_stream(dev).synchronize()  # zeroed for every stream from here on
+        ws = _SharedStatus(dev)
+        if not torch.cuda.is_current_stream_capturing():
             _status_ws[dev.index] = ws
     return ws
 
 
 def fp8_status(device=None, clear: bool = False) -> tuple[int, int]:
     """Synchronise the current stream and return (status, detail) of the 8-bit
-    products that were given no workspace on this device (but for those captured
-    into a graph before the first eager one).  An error stays until `clear`."""
+    products that were given no workspace on this device.  An error stays until
+    `clear`."""
     dev = torch.device("cuda" if device is None else device)
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())

@@ -213,10 +213,27 @@ coda_status rms8_bwd(const RmsBwdParams& p, void* stream) {
   return launch_pass(CODA_KERNEL_RMSNORM_FP8_BWD, rmsnorm_fp8_bwd_kernel<T, CH>, rms8_bwd_ctas(p.M, p.d), T, stream, p);
 }
 
+// The status word of calls that bring no workspace, one per device.
+__device__ __align__(256) unsigned char g_shared_status[kStatusBytes];
+std::atomic<void*> g_shared_status_addr[kMaxDevices];
+
 }  // namespace
 }  // namespace coda
 
 extern "C" {
+
+coda_status coda_shared_status(void** ws) {
+  if (ws == nullptr) return CODA_ERR_INVALID_ARG;
+  int dev;
+  CODA_TRY(current_device(dev));
+  void* p = g_shared_status_addr[dev].load();
+  if (p == nullptr) {
+    if (cudaGetSymbolAddress(&p, g_shared_status) != cudaSuccess || p == nullptr) return CODA_ERR_CUDA;
+    g_shared_status_addr[dev].store(p);
+  }
+  *ws = p;
+  return CODA_OK;
+}
 
 coda_status coda_selftest_fp8_silence(int role, int cta) {
   if (role < 0 || role > CODA_FP8_ROLE_SCALES || cta < 0 || cta >= 1 << 20) return CODA_ERR_INVALID_ARG;

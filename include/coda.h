@@ -82,6 +82,13 @@ coda_status coda_status_clear(void* ws, void* stream);
  * 32-bit detail word (kernel id << 16 | role << 8 | reason). */
 coda_status coda_status_query(const void* ws, void* stream, uint32_t* detail);
 
+/* The current device's status word for products that bring no workspace of
+ * their own: coda_gemm_workspace_bytes() bytes of the library, zero when it is
+ * loaded, at the same address for the whole process.  To be passed as `ws` (also
+ * while a stream is being captured), read with coda_status_query and cleared
+ * with coda_status_clear; an error stays until it is cleared. */
+coda_status coda_shared_status(void** ws);
+
 /* Set the per-wait limit of device-side bounded waits, in nanoseconds, for
  * launches issued after this call from any host thread (default 4e9 = 4 s).
  * Values are clamped to [1e3, 6e10]. */

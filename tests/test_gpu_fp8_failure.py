@@ -145,3 +145,89 @@ def test_shared_tile_of_which_a_part_is_missing_is_not_stored(cuda_lib, name, ro
 def test_few_rows_of_which_a_part_is_missing_are_not_stored(cuda_lib, name, M, K, role, cta):
     """The same for the CTAs that share the reduction of a product of few rows."""
     _run(cuda_lib, name, role, cta, _few_rows_tile(name), M=M, N=256, K=K)
+
+
+def _product(B, seed=1):
+    x, w = B.quant_fp8(_bf(40, 256, seed=seed)), B.quant_fp8_blocks(_bf(64, 256, seed=seed + 1))
+    return lambda **kw: B.gemm_fp8(x["Qr"], x["Sr"], w["Q"], w["S"], 40, 64, 256, **kw)
+
+
+def test_status_of_products_captured_before_the_first_eager_one(cuda_lib):
+    """All products without a workspace share one word, which fp8_status reads: captured ones too."""
+    B = cuda_lib
+    dev = torch.device("cuda", torch.cuda.current_device())
+    word = B._status_workspace(dev).buf.data_ptr()
+    call = _product(B)
+    want = call()
+    out = torch.zeros_like(want)
+    kept = dict(B._status_ws)
+    B._status_ws.clear()
+    try:
+        graphs = [torch.cuda.CUDAGraph() for _ in range(3)]
+        for i, g in enumerate(graphs):
+            with contextlib.ExitStack() as stack:
+                if i == 1:
+                    stack.enter_context(silence(B, MMA, 0))
+                stack.enter_context(torch.cuda.graph(g))
+                call(out=out)
+        graphs[0].replay()
+        assert B.fp8_status() == (0, 0) and torch.equal(out, want)
+        graphs[1].replay()
+        assert B.fp8_status()[0] == TIMEOUT
+        graphs[2].replay()
+        assert B.fp8_status(clear=True)[0] == TIMEOUT and torch.equal(out, want)   # it stays until cleared
+        graphs[2].replay()
+        assert B.fp8_status() == (0, 0)
+        assert B._status_workspace(dev).buf.data_ptr() == word
+    finally:
+        B._status_ws.clear()
+        B._status_ws.update(kept)
+
+
+def test_status_word_of_first_calls_on_several_threads(cuda_lib):
+    import threading
+    B = cuda_lib
+    dev = torch.device("cuda", torch.cuda.current_device())
+    kept = dict(B._status_ws)
+    B._status_ws.clear()
+    try:
+        start, seen = threading.Barrier(8), []
+
+        def first():
+            start.wait()
+            seen.append(B._status_workspace(dev).buf.data_ptr())
+        threads = [threading.Thread(target=first) for _ in range(8)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        B._status_ws.clear()
+        assert len(seen) == 8 and set(seen) == {B._status_workspace(dev).buf.data_ptr()}
+    finally:
+        B._status_ws.clear()
+        B._status_ws.update(kept)
+
+
+FIRST = """
+import torch
+from gemm_epilogue_fusion_tmem_b200 import binding as B
+e4 = torch.float8_e4m3fn
+a, w = torch.ones(40, 256, device="cuda").to(e4), torch.ones(64, 256, device="cuda").to(e4)
+sa, sw = torch.ones(2, 40, device="cuda"), torch.ones(1, 2, device="cuda")
+out = torch.zeros(40, 64, device="cuda", dtype=torch.bfloat16)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    B.gemm_fp8(a, sa, w, sw, 40, 64, 256, out=out)
+g.replay()
+assert B.fp8_status() == (0, 0) and (out == 256).all()
+print("captured first")
+"""
+
+
+def test_the_first_call_of_a_process_may_be_captured(cuda_lib):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "captured first" in run.stdout, run.stderr[-2000:]
