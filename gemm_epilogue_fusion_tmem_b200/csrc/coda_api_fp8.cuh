@@ -136,14 +136,14 @@ coda_status launch_gemm8_majors(const CUtensorMap& ta, const CUtensorMap& tb, bo
 
 // Tiles of the few-rows kernel: 128 weight rows (and their partners in the up
 // half) x up to TN rows of A, split over k by a cluster.
-template <int TN, bool SWIGLU>
-coda_status launch_skinny8(const CUtensorMap& tw, const CUtensorMap& tx, Skinny8Params p, cudaStream_t s) {
+template <int TN, bool SWIGLU, bool SELFTEST>
+coda_status launch_skinny8_as(const CUtensorMap& tw, const CUtensorMap& tx, Skinny8Params p, cudaStream_t s) {
   using C = F8SkinnyCfg<TN, SWIGLU>;
   static std::atomic<bool> ready[kMaxDevices];
   int dev = 0;
   coda_status st = current_device(dev);
   if (st != CODA_OK) return st;
-  auto kern = gemm_fp8_skinny_kernel<TN, SWIGLU>;
+  auto kern = gemm_fp8_skinny_kernel<TN, SWIGLU, SELFTEST>;
   if (!ready[dev].load()) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
       return CODA_ERR_CUDA;
@@ -161,6 +161,12 @@ coda_status launch_skinny8(const CUtensorMap& tw, const CUtensorMap& tx, Skinny8
       launch_ex(kern, dim3(tiles * splits), dim3(F8S_THREADS), C::SMEM_BYTES, s, splits, tw, tx, p);
   g_launch_tag = -1;
   return e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess ? CODA_OK : CODA_ERR_CUDA;
+}
+
+template <int TN, bool SWIGLU>
+coda_status launch_skinny8(const CUtensorMap& tw, const CUtensorMap& tx, const Skinny8Params& p, cudaStream_t s) {
+  return g_fp8_silent ? launch_skinny8_as<TN, SWIGLU, true>(tw, tx, p, s)
+                      : launch_skinny8_as<TN, SWIGLU, false>(tw, tx, p, s);
 }
 
 inline bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
