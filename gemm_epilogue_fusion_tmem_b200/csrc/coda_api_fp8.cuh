@@ -13,6 +13,9 @@ namespace {
 thread_local uint32_t g_fp8_silent = 0;
 
 constexpr int kScaleBlock = 128;  // values per scale along a blocked axis
+// Rows of every matrix (and K of the products): row numbers of a partial last tile, and
+// those one step of a grid further, are still ints.
+constexpr int kMax8Rows = 0x7FFFFFFF - 4095;
 constexpr int kMax8Cols = 1 << 22;  // columns of the light passes' matrices: 32-bit offsets in a 128-row tile
 
 // 8-bit matrix [rows][cols], boxes of box_cols x box_rows; out-of-range elements load as zero.
@@ -255,7 +258,8 @@ coda_status coda_quant_fp8(const void* X, const float* rowvec_or_null, const voi
   const bool rows = Qr_or_null != nullptr || Sr_or_null != nullptr;
   const bool cols = Qc_or_null != nullptr || Sc_or_null != nullptr;
   if (R < 0 || C < 1 || !known_format(format)) return CODA_ERR_INVALID_ARG;
-  if (C % 16 != 0 || C > kMax8Cols || !tiles_fit(cdiv(R, kScaleBlock), cdiv(C, kScaleBlock))) return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (C % 16 != 0 || C > kMax8Cols || R > kMax8Rows || !tiles_fit(cdiv(R, kScaleBlock), cdiv(C, kScaleBlock)))
+    return CODA_ERR_UNSUPPORTED_SHAPE;
   if (R == 0) return CODA_OK;
   if (!X || (!rows && !cols)) return CODA_ERR_INVALID_ARG;
   if (rows && (!Qr_or_null || !Sr_or_null)) return CODA_ERR_INVALID_ARG;
@@ -284,7 +288,8 @@ coda_status coda_quant_fp8(const void* X, const float* rowvec_or_null, const voi
 
 coda_status coda_quant_fp8_blocks(const void* W, void* Q, float* S, int R, int C, int format, void* stream) {
   if (R < 0 || C < 1 || !known_format(format)) return CODA_ERR_INVALID_ARG;
-  if (C % 16 != 0 || C > kMax8Cols || !tiles_fit(cdiv(R, kScaleBlock), cdiv(C, kScaleBlock))) return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (C % 16 != 0 || C > kMax8Cols || R > kMax8Rows || !tiles_fit(cdiv(R, kScaleBlock), cdiv(C, kScaleBlock)))
+    return CODA_ERR_UNSUPPORTED_SHAPE;
   if (R == 0) return CODA_OK;
   if (!W || !Q || !S) return CODA_ERR_INVALID_ARG;
   if (!aligned16(W) || !aligned16(Q) || !aligned16(S)) return CODA_ERR_MISALIGNED;
@@ -315,7 +320,8 @@ coda_status coda_gemm_fp8(const void* A, const float* SA, const void* B, const f
   if (accumulate && !c_fp32) return CODA_ERR_INVALID_ARG;
   if (M == 0 || N == 0) return CODA_OK;  // empty output
   if (N % 16 != 0 || (a_mn_major ? M : K) % 16 != 0 || (!b_mn_major && K % 16 != 0)) return CODA_ERR_UNSUPPORTED_SHAPE;
-  if (!tiles_fit(cdiv(M, 256), cdiv(N, 256))) return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (M > kMax8Rows || N > kMax8Rows || K > kMax8Rows || !tiles_fit(cdiv(M, 256), cdiv(N, 256)))
+    return CODA_ERR_UNSUPPORTED_SHAPE;
   if (K == 0) {  // empty sums
     if (!C) return CODA_ERR_INVALID_ARG;
     return accumulate ? CODA_OK : zero_fill({{C, (size_t)M * N * (c_fp32 ? 4 : 2)}}, stream);
@@ -381,7 +387,8 @@ coda_status coda_gemm_swiglu_fp8(const void* A, const float* SA, const void* Wgu
                                  void* AB_or_null, float* SAB_or_null, int M, int K, int F, void* ws, size_t ws_bytes,
                                  void* stream) {
   if (M < 0 || K < 1 || F < 1) return CODA_ERR_INVALID_ARG;
-  if (K % 16 != 0 || F % kScaleBlock != 0 || F > kMax8Cols || !tiles_fit(cdiv(M, 256), F / kScaleBlock))
+  if (K % 16 != 0 || F % kScaleBlock != 0 || F > kMax8Cols || M > kMax8Rows || K > kMax8Rows ||
+      !tiles_fit(cdiv(M, 256), F / kScaleBlock))
     return CODA_ERR_UNSUPPORTED_SHAPE;
   if (M == 0) return CODA_OK;
   if (!A || !SA || !Wgu || !SW || !Y || !SY || !ws) return CODA_ERR_INVALID_ARG;
@@ -446,7 +453,7 @@ coda_status coda_swiglu_fp8_bwd(const void* dY, const void* AB, const float* SAB
                                 void* dAc_or_null, float* SdAc_or_null, void* Yc_or_null, float* SYc_or_null, int M,
                                 int F, int format, void* stream) {
   if (M < 0 || F < 1 || !known_format(format)) return CODA_ERR_INVALID_ARG;
-  if (F % kScaleBlock != 0 || F > kMax8Cols || !tiles_fit(cdiv(M, kScaleBlock), F / kScaleBlock))
+  if (F % kScaleBlock != 0 || F > kMax8Cols || M > kMax8Rows || !tiles_fit(cdiv(M, kScaleBlock), F / kScaleBlock))
     return CODA_ERR_UNSUPPORTED_SHAPE;
   if (M == 0) return CODA_OK;
   if (!dY || !AB || !SAB || !dA || !SdA) return CODA_ERR_INVALID_ARG;
@@ -485,7 +492,7 @@ coda_status coda_swiglu_fp8_bwd(const void* dY, const void* AB, const float* SAB
 coda_status coda_rmsnorm_fp8_fwd(const void* X, const void* R_or_null, const void* g, void* H_or_null, float* r,
                                  void* Q, float* S, int M, int d, float eps, void* stream) {
   if (M < 0 || d < 1 || !(eps > 0.f)) return CODA_ERR_INVALID_ARG;
-  if (d % 16 != 0 || d > kRms8MaxD) return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (d % 16 != 0 || d > kRms8MaxD || M > kMax8Rows) return CODA_ERR_UNSUPPORTED_SHAPE;
   if (M == 0) return CODA_OK;
   if (!X || !g || !r || !Q || !S || (R_or_null == nullptr) != (H_or_null == nullptr)) return CODA_ERR_INVALID_ARG;
   const void* ptrs[] = {X, R_or_null, g, H_or_null, r, Q, S};
@@ -523,7 +530,7 @@ coda_status coda_rmsnorm_fp8_bwd(const void* dN, const void* H, const float* r, 
                                  const void* dH_in_or_null, void* dH, float* dg, int M, int d, void* ws,
                                  size_t ws_bytes, void* stream) {
   if (M < 0 || d < 1) return CODA_ERR_INVALID_ARG;
-  if (d % 16 != 0 || d > kRms8MaxD) return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (d % 16 != 0 || d > kRms8MaxD || M > kMax8Rows) return CODA_ERR_UNSUPPORTED_SHAPE;
   if (M == 0) return zero_fill({{dg, (size_t)d * 4}}, stream);
   if (!dN || !H || !r || !g || !dH || !dg || !ws) return CODA_ERR_INVALID_ARG;
   const void* ptrs[] = {dN, H, r, g, dH_in_or_null, dH, dg, ws};

@@ -394,7 +394,8 @@ coda_status coda_qkv_rope_bwd(const void* dQKV, const void* X, const void* Wqkv,
  * a weight gradient dY^T X takes dY and X as they are stored, in columns form.
  *
  * Quantised matrices are dense, their column count a multiple of 16 (at most
- * 2^22 in the passes other than coda_gemm_fp8); any number of rows.  Outputs may
+ * 2^22 in the passes other than coda_gemm_fp8), their rows (and M, N and K) at
+ * most 2^31 - 4096; more is CODA_ERR_UNSUPPORTED_SHAPE.  Outputs may
  * not overlap inputs.  These calls allocate nothing and, but for the norm's
  * backward, need no scratch; `ws` of the two products holds only the status word. */
 #define CODA_FP8_E4M3 0

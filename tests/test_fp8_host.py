@@ -165,3 +165,21 @@ def test_format_codes_match_the_header():
                        ("QUANT_FP8", B.KERNEL_QUANT_FP8), ("SWIGLU_FP8_BWD", B.KERNEL_SWIGLU_FP8_BWD),
                        ("RMSNORM_FP8_FWD", B.KERNEL_RMSNORM_FP8_FWD), ("RMSNORM_FP8_BWD", B.KERNEL_RMSNORM_FP8_BWD)):
         assert f"#define CODA_KERNEL_{name} {code} " in src
+
+
+def test_row_limits():
+    """Row numbers of a last tile, or one step of a grid further, stay below 2^31: more rows are refused."""
+    lib, top, over = B.library(), 2 ** 31 - 4096, 2 ** 31 - 4095
+    for bad in (dict(M=over, N=16), dict(M=16, N=2 ** 31 - 16), dict(M=16, N=16, K=2 ** 31 - 16),
+                dict(a_mn=1, b_mn=1, blocks=0, M=2 ** 31 - 16, N=16)):
+        assert _gemm(**bad) == 2, bad
+    assert _gemm(M=top, N=16, wsb=0) == 4   # the limit itself passes the checks of shapes
+    assert lib.coda_gemm_swiglu_fp8._fn(*[ONE] * 8, over, 16, 128, ONE, 256, None) == 2
+    assert lib.coda_gemm_swiglu_fp8._fn(*[ONE] * 8, 16, 2 ** 31 - 16, 128, ONE, 256, None) == 2
+    assert lib.coda_gemm_swiglu_fp8._fn(*[ONE] * 8, top, 16, 128, ONE, 0, None) == 4
+    assert lib.coda_quant_fp8._fn(ONE, None, None, ONE, ONE, ONE, ONE, over, 16, 0, None) == 2
+    assert lib.coda_quant_fp8._fn(P(8), None, None, ONE, ONE, ONE, ONE, top, 16, 0, None) == 3
+    assert lib.coda_quant_fp8_blocks._fn(ONE, ONE, ONE, over, 16, 0, None) == 2
+    assert lib.coda_swiglu_fp8_bwd._fn(*[ONE] * 9, over, 128, 0, None) == 2
+    assert lib.coda_rmsnorm_fp8_fwd._fn(*[ONE] * 7, over, 16, 1e-6, None) == 2
+    assert lib.coda_rmsnorm_fp8_bwd._fn(*[ONE] * 7, over, 16, ONE, BIG, None) == 2
