@@ -702,13 +702,21 @@ def _fp8(dtype, name: str) -> int:
     return _FP8[dtype]
 
 
+def _no_int(*sizes) -> None:
+    """Refuse sizes of which one is no C int (ctypes would cut it down to one)."""
+    raise ValueError(f"sizes must be from 0 to 2^31 - 1, got {sizes}")
+
+
 def _req2(t, name: str) -> tuple:
     """Rows and columns of the matrix that fixes an entry point's sizes."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
-    return tuple(t.shape)
+    R, C = t.shape
+    if (R | C) >> 31:
+        _no_int(R, C)
+    return R, C
 
 
 def _in(t, name: str, dtype, shape, dev=None):
@@ -837,6 +845,8 @@ def gemm_fp8(A, SA, B, SB, M: int, N: int, K: int, a_mn_major: bool = False, b_m
     if not (isinstance(A, torch.Tensor) and isinstance(B, torch.Tensor)):
         raise TypeError("A and B must be torch.Tensors")
     fa, fb = _fp8(A.dtype, "A"), _fp8(B.dtype, "B")
+    if (M | N | K) >> 31:
+        _no_int(M, N, K)
     dev = A.device
     kb, nb = _cdiv(K, 128), _cdiv(N, 128)
     a = _in(A, "A", A.dtype, (K, M) if a_mn_major else (M, K))

@@ -183,3 +183,19 @@ def test_row_limits():
     assert lib.coda_swiglu_fp8_bwd._fn(*[ONE] * 9, over, 128, 0, None) == 2
     assert lib.coda_rmsnorm_fp8_fwd._fn(*[ONE] * 7, over, 16, 1e-6, None) == 2
     assert lib.coda_rmsnorm_fp8_bwd._fn(*[ONE] * 7, over, 16, ONE, BIG, None) == 2
+
+
+def test_sizes_that_are_no_c_int_are_refused():
+    """2^32 + 5 rows would be passed on as 5."""
+    n, e4 = 2 ** 32 + 5, torch.float8_e4m3fn
+    t = lambda *s, dtype=e4: torch.empty(*s, dtype=dtype, device="meta")
+    bf = torch.bfloat16
+    for call in (lambda: B.gemm_fp8(t(n, 16), t(1, n), t(16, 16), t(1, 1), n, 16, 16),
+                 lambda: B.gemm_fp8(t(0, 16), t(1, 0), t(16, 16), t(1, 1), -1, 16, 16),
+                 lambda: B.quant_fp8(t(n, 16, dtype=bf)), lambda: B.quant_fp8_blocks(t(n, 16, dtype=bf)),
+                 lambda: B.gemm_swiglu_fp8(t(n, 16), t(1, n), t(256, 16), t(2, 1)),
+                 lambda: B.swiglu_fp8_bwd(t(n, 128, dtype=bf), t(n, 256), t(2, n)),
+                 lambda: B.rmsnorm_fp8_fwd(t(n, 16, dtype=bf), t(16, dtype=bf), 1e-6),
+                 lambda: B.rmsnorm_fp8_bwd(t(n, 16, dtype=bf), t(n, 16, dtype=bf), t(n), t(16, dtype=bf))):
+        with pytest.raises(ValueError, match="sizes must be from 0"):
+            call()
