@@ -729,6 +729,12 @@ def _in(t, name: str, dtype, shape, dev=None):
     return t.data_ptr()
 
 
+def _ws_on(ws: Workspace, dev) -> Workspace:
+    if ws.buf.device != dev:
+        raise ValueError(f"ws is on {ws.buf.device}, the tensors on {dev}")
+    return ws
+
+
 def _new(shape: tuple, dtype, dev):
     """A new dense vector or matrix (empty_strided: a third less host time than new_empty)."""
     return torch.empty_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype=dtype, device=dev)
@@ -862,7 +868,7 @@ def gemm_fp8(A, SA, B, SB, M: int, N: int, K: int, a_mn_major: bool = False, b_m
         c = C.data_ptr()
     else:
         C, c = out, _in(out, "C", out_dtype, (M, N), dev)
-    ws = ws or _status_workspace(dev)
+    ws = _status_workspace(dev) if ws is None else _ws_on(ws, dev)
     _call("coda_gemm_fp8", dev, a, sa, b, sb, c, M, N, K, int(a_mn_major), int(b_mn_major), fa, fb, int(b_blocks),
           int(out_dtype == torch.float32), int(accumulate), ws.buf.data_ptr(), ws.nbytes)
     return C
@@ -889,7 +895,7 @@ def gemm_swiglu_fp8(A, SA, Wgu, SW, save_ab: bool = True, out: dict | None = Non
     ab = sab = None
     if save_ab:
         ab, sab = _out(o, "AB", (M, 2 * F), e4m3, dev), _out(o, "SAB", (2 * fb, M), torch.float32, dev)
-    ws = ws or _status_workspace(dev)
+    ws = _status_workspace(dev) if ws is None else _ws_on(ws, dev)
     _call("coda_gemm_swiglu_fp8", dev, a, sa, w, sw, y, sy, ab, sab, M, K, F, ws.buf.data_ptr(), ws.nbytes)
     return o
 
@@ -950,6 +956,6 @@ def rmsnorm_fp8_bwd(dN, H, r, g, dH_in=None, out: dict | None = None, ws: Worksp
     hi = None if dH_in is None else _in(dH_in, "dH_in", bf16, (M, d), dev)
     o = dict(out or {})
     dh, dg = _out(o, "dH", (M, d), bf16, dev), _out(o, "dg", (d,), torch.float32, dev)
-    buf = ws.buf if ws is not None else _new((lib.coda_rmsnorm_fp8_bwd_workspace_bytes(M, d),), torch.uint8, dev)
+    buf = _ws_on(ws, dev).buf if ws is not None else _new((lib.coda_rmsnorm_fp8_bwd_workspace_bytes(M, d),), torch.uint8, dev)
     _call("coda_rmsnorm_fp8_bwd", dev, dn, h, rp, gp, hi, dh, dg, M, d, buf.data_ptr(), buf.numel())
     return o

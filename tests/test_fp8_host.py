@@ -199,3 +199,11 @@ def test_sizes_that_are_no_c_int_are_refused():
                  lambda: B.rmsnorm_fp8_bwd(t(n, 16, dtype=bf), t(n, 16, dtype=bf), t(n), t(16, dtype=bf))):
         with pytest.raises(ValueError, match="sizes must be from 0"):
             call()
+
+
+def test_workspace_must_lie_where_the_tensors_do():
+    """A kernel that is given host memory, or another device's, as its scratch would fault."""
+    cpu, dev = B.Workspace(256, "cpu"), torch.device("cuda", 0)
+    with pytest.raises(ValueError, match="ws is on cpu"):
+        B._ws_on(cpu, dev)
+    assert B._ws_on(cpu, torch.device("cpu")) is cpu

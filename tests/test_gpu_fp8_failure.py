@@ -231,3 +231,16 @@ def test_the_first_call_of_a_process_may_be_captured(cuda_lib):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     run = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
     assert run.returncode == 0 and "captured first" in run.stdout, run.stderr[-2000:]
+
+
+def test_workspaces_of_another_device_are_refused(cuda_lib):
+    B = cuda_lib
+    ws = B.Workspace(1 << 20, "cpu")
+    with pytest.raises(ValueError, match="ws is on cpu"):
+        _product(B)(ws=ws)
+    x, w = B.quant_fp8(_bf(40, 256, seed=1)), B.quant_fp8_blocks(_bf(256, 256, seed=2))
+    with pytest.raises(ValueError, match="ws is on cpu"):
+        B.gemm_swiglu_fp8(x["Qr"], x["Sr"], w["Q"], w["S"], ws=ws)
+    h = _bf(4, 256, seed=3)
+    with pytest.raises(ValueError, match="ws is on cpu"):
+        B.rmsnorm_fp8_bwd(h, h, torch.ones(4, device="cuda"), h[0], ws=ws)
