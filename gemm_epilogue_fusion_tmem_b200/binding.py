@@ -99,6 +99,7 @@ def library() -> ctypes.CDLL:
             "coda_quant_fp8": (I, [P] * 7 + [I, I, I, P]),
             "coda_quant_fp8_blocks": (I, [P, P, P, I, I, I, P]),
             "coda_gemm_fp8": (I, [P] * 5 + [I] * 10 + [P, S, P]),
+            "coda_gemm_fp8_parts": (I, [I] * 7 + [ctypes.POINTER(I)] * 2),
             "coda_gemm_swiglu_fp8": (I, [P] * 8 + [I, I, I, P, S, P]),
             "coda_swiglu_fp8_bwd": (I, [P] * 9 + [I, I, I, P]),
             "coda_rmsnorm_fp8_fwd": (I, [P] * 7 + [I, I, F, P]),
@@ -118,7 +119,7 @@ def library() -> ctypes.CDLL:
 # Host-side entry points that enqueue no GPU work get no NVTX range.
 _UNRANGED = {"coda_status_string", "coda_version", "coda_set_wait_limit_ns", "coda_profile_arm",
              "coda_status_query", "coda_static_status_query", "coda_selftest_fp8_silence",
-             "coda_shared_status"}
+             "coda_shared_status", "coda_gemm_fp8_parts"}
 
 
 class _Ranged:
@@ -872,6 +873,19 @@ def gemm_fp8(A, SA, B, SB, M: int, N: int, K: int, a_mn_major: bool = False, b_m
     _call("coda_gemm_fp8", dev, a, sa, b, sb, c, M, N, K, int(a_mn_major), int(b_mn_major), fa, fb, int(b_blocks),
           int(out_dtype == torch.float32), int(accumulate), ws.buf.data_ptr(), ws.nbytes)
     return C
+
+
+def gemm_fp8_parts(M: int, N: int, K: int, a_mn_major: bool = False, b_mn_major: bool = False, b_blocks: bool = True,
+                   out_dtype=torch.bfloat16) -> tuple[bool, int]:
+    """(few rows' kernel, CTAs or CTA pairs that share each tile's reduction) of such a product on the current
+    device; see coda_gemm_fp8_parts."""
+    few, parts = _c_int(0), _c_int(0)
+    if (M | N | K) >> 31:
+        _no_int(M, N, K)
+    _check(library().coda_gemm_fp8_parts(M, N, K, int(a_mn_major), int(b_mn_major), int(b_blocks),
+                                         int(out_dtype == torch.float32), ctypes.byref(few), ctypes.byref(parts)),
+           "coda_gemm_fp8_parts")
+    return bool(few.value), parts.value
 
 
 def gemm_swiglu_fp8(A, SA, Wgu, SW, save_ab: bool = True, out: dict | None = None,

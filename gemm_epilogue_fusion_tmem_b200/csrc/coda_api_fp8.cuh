@@ -113,14 +113,20 @@ coda_status launch_gemm8(const CUtensorMap& ta, const CUtensorMap& tb, Gemm8Para
 // 13.8 and 14.7.
 // Weight gradients have a tile per 256 x 256 of the weight and fill the device.
 template <int EPI, bool B_MN>
-coda_status launch_gemm8_activation(const CUtensorMap& ta, const CUtensorMap& tb, const Gemm8Params& p, cudaStream_t s) {
-  const long long tiles = (long long)p.num_m_tiles * p.num_n_tiles;
-  for (int parts = 4; parts > 1; --parts) {
-    if (tiles * 2 * parts > num_sms() || p.k_blocks - cdiv(p.k_blocks, parts) < 12) continue;
+coda_status activation_parts(long long tiles, int k_blocks, int& parts) {
+  for (parts = 4; parts > 1; --parts) {
+    if (tiles * 2 * parts > num_sms() || k_blocks - cdiv(k_blocks, parts) < 12) continue;
     int clusters = 0;
     CODA_TRY((gemm8_clusters<EPI, false, B_MN, false, true>(parts, clusters)));
-    if (tiles <= clusters) return launch_gemm8<EPI, false, B_MN, false, true>(ta, tb, p, s, parts);
+    if (tiles <= clusters) return CODA_OK;
   }
+  return CODA_OK;  // 1: not shared
+}
+template <int EPI, bool B_MN>
+coda_status launch_gemm8_activation(const CUtensorMap& ta, const CUtensorMap& tb, const Gemm8Params& p, cudaStream_t s) {
+  int parts = 1;
+  CODA_TRY((activation_parts<EPI, B_MN>((long long)p.num_m_tiles * p.num_n_tiles, p.k_blocks, parts)));
+  if (parts > 1) return launch_gemm8<EPI, false, B_MN, false, true>(ta, tb, p, s, parts);
   return launch_gemm8<EPI, false, B_MN, false>(ta, tb, p, s);
 }
 
@@ -135,6 +141,14 @@ coda_status launch_gemm8_majors(const CUtensorMap& ta, const CUtensorMap& tb, bo
   }
   if (a_mn && b_mn) return launch_gemm8<EPI, true, true, VEC>(ta, tb, p, s);
   return launch_gemm8<EPI, true, false, VEC>(ta, tb, p, s);
+}
+
+// CTAs that share the reduction of a tile of the few-rows kernel: doubled while there
+// are two CTAs per SM to be had and two blocks of k for each.
+inline int skinny8_splits(int tiles, int k_blocks) {
+  int splits = 1;
+  while (splits < 8 && tiles * splits * 2 <= 2 * num_sms() && splits * 4 <= k_blocks) splits *= 2;
+  return splits;
 }
 
 // Tiles of the few-rows kernel: 128 weight rows (and their partners in the up
@@ -153,8 +167,7 @@ coda_status launch_skinny8_as(const CUtensorMap& tw, const CUtensorMap& tx, Skin
     ready[dev].store(true);
   }
   const int tiles = cdiv(p.N, 128);
-  int splits = 1;  // doubled while there are two CTAs per SM to be had and two blocks of k for each
-  while (splits < 8 && tiles * splits * 2 <= 2 * g_dev[dev].num_sms && splits * 4 <= p.k_blocks) splits *= 2;
+  const int splits = skinny8_splits(tiles, p.k_blocks);
   p.idesc = (p.idesc & ~(0x3Fu << 17)) | ((uint32_t)(TN >> 3) << 17);
   p.wait_limit_ns = g_wait_limit_ns.load();
   p.silent = std::exchange(g_fp8_silent, 0u);
@@ -171,6 +184,9 @@ coda_status launch_skinny8(const CUtensorMap& tw, const CUtensorMap& tx, const S
   return g_fp8_silent ? launch_skinny8_as<TN, SWIGLU, true>(tw, tx, p, s)
                       : launch_skinny8_as<TN, SWIGLU, false>(tw, tx, p, s);
 }
+
+// Few rows of an activation by a weight as it is stored.
+inline bool gemm8_few_rows(int M, bool a_mn, bool b_mn, bool b_blocks) { return M <= 64 && !a_mn && !b_mn && b_blocks; }
 
 inline bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 inline bool known_format(int f) { return f == CODA_FP8_E4M3 || f == CODA_FP8_E5M2; }
@@ -336,7 +352,7 @@ coda_status coda_gemm_fp8(const void* A, const float* SA, const void* B, const f
   const bool a_mn = a_mn_major != 0, b_mn = b_mn_major != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   CUtensorMap ta, tb;
-  if (M <= 64 && !a_mn && !b_mn && b_blocks) {
+  if (gemm8_few_rows(M, a_mn, b_mn, b_blocks != 0)) {
     const int tn = skinny8_rows(M);
     if (!operand8_map(&tb, B, N, K, false, 128) || !operand8_map(&ta, A, M, K, false, tn)) return CODA_ERR_CUDA;
     Skinny8Params p;
@@ -381,6 +397,26 @@ coda_status coda_gemm_fp8(const void* A, const float* SA, const void* B, const f
                     : launch_gemm8_majors<F8_EPI_F32, true>(ta, tb, a_mn, b_mn, p, s);
   return b_blocks ? launch_gemm8_majors<F8_EPI_BF16, false>(ta, tb, a_mn, b_mn, p, s)
                   : launch_gemm8_majors<F8_EPI_BF16, true>(ta, tb, a_mn, b_mn, p, s);
+}
+
+coda_status coda_gemm_fp8_parts(int M, int N, int K, int a_mn_major, int b_mn_major, int b_blocks, int c_fp32,
+                                int* few_rows, int* parts) {
+  if (M < 1 || N < 1 || K < 1 || few_rows == nullptr || parts == nullptr) return CODA_ERR_INVALID_ARG;
+  int dev;
+  CODA_TRY(current_device(dev));
+  *few_rows = gemm8_few_rows(M, a_mn_major != 0, b_mn_major != 0, b_blocks != 0);
+  *parts = 1;
+  const int k_blocks = cdiv(K, F8_BK);
+  const long long tiles = (long long)cdiv(M, 256) * cdiv(N, 256);
+  if (*few_rows) {
+    *parts = skinny8_splits(cdiv(N, 128), k_blocks);
+    return CODA_OK;
+  }
+  if (a_mn_major || !b_blocks) return CODA_OK;
+  if (c_fp32) return b_mn_major ? activation_parts<F8_EPI_F32, true>(tiles, k_blocks, *parts)
+                                : activation_parts<F8_EPI_F32, false>(tiles, k_blocks, *parts);
+  return b_mn_major ? activation_parts<F8_EPI_BF16, true>(tiles, k_blocks, *parts)
+                    : activation_parts<F8_EPI_BF16, false>(tiles, k_blocks, *parts);
 }
 
 coda_status coda_gemm_swiglu_fp8(const void* A, const float* SA, const void* Wgu, const float* SW, void* Y, float* SY,

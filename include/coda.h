@@ -428,6 +428,12 @@ coda_status coda_gemm_fp8(const void* A, const float* SA, const void* B, const f
                           int a_mn_major, int b_mn_major, int a_format, int b_format, int b_blocks, int c_fp32,
                           int accumulate, void* ws, size_t ws_bytes, void* stream);
 
+/* How coda_gemm_fp8 forms such a product on the current device: *few_rows 1 for the
+ * kernel whose tiles are 128 columns of C, 0 for tiles of 256 x 256; *parts CTAs, or
+ * CTA pairs, share the reduction of each tile (1: none is shared).  Nothing is launched. */
+coda_status coda_gemm_fp8_parts(int M, int N, int K, int a_mn_major, int b_mn_major, int b_blocks, int c_fp32,
+                                int* few_rows, int* parts);
+
 /* coda_gemm_swiglu on 8-bit operands: [a | b] = A Wgu^T, Y = silu(a) * b, all e4m3.
  * A [M, K] in rows form, Wgu [2F, K] (gate rows first) in blocks form.  Outputs
  * Y [M, F] in rows form, SY [F/128, M] (the down projection's operand), and the

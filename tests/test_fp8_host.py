@@ -207,3 +207,13 @@ def test_workspace_must_lie_where_the_tensors_do():
     with pytest.raises(ValueError, match="ws is on cpu"):
         B._ws_on(cpu, dev)
     assert B._ws_on(cpu, torch.device("cpu")) is cpu
+
+
+def test_parts_refusals():
+    few, parts = ctypes.c_int(0), ctypes.c_int(0)
+    fn = B.library().coda_gemm_fp8_parts
+    for bad in ((0, 16, 16), (16, -1, 16), (16, 16, 0)):
+        assert fn(*bad, 0, 0, 1, 0, ctypes.byref(few), ctypes.byref(parts)) == 1, bad
+    assert fn(16, 16, 16, 0, 0, 1, 0, None, ctypes.byref(parts)) == 1
+    with pytest.raises(ValueError, match="sizes must be"):
+        B.gemm_fp8_parts(2 ** 31, 16, 16)

@@ -237,6 +237,40 @@ def test_gemm_reduction_shared_by_pairs(cuda_lib, M, N, K, b_mn, f32):
         check_close(num(C), want, err + FP32 * (np.abs(want) + err), "added")
 
 
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("parts,N,K,b_mn", [(4, 256, 2320, False), (3, 256, 2320, False), (3, 256, 2320, True), (2, 512, 4096, True),
+                                            (2, 256, 3088, False), (1, 256, 2320, False)])
+def test_gemm_reduction_shared_by_a_known_number_of_pairs(cuda_lib, parts, N, K, b_mn, f32):
+    """The most tiles that this device shares between `parts` pairs (shares of 32, of 42 and 43, of 64 rows each),
+    as the library says; one part: the fewest tiles that are not shared."""
+    dtype = torch.float32 if f32 else torch.bfloat16
+    how = lambda m: cuda_lib.gemm_fp8_parts(256 * m, N, K, b_mn_major=b_mn, out_dtype=dtype)
+    tiles = [m for m in range(1, 80) if how(m) == (False, parts)]
+    assert tiles, [how(m) for m in range(1, 80)]
+    M = 256 * (tiles[0] if parts == 1 else tiles[-1]) - 39   # a short last tile
+    assert cuda_lib.gemm_fp8_parts(M, N, K, b_mn_major=b_mn, out_dtype=dtype) == (False, parts)
+    args, kw, ref, err = _gemm_case(cuda_lib, M, N, K, False, b_mn, True, "e4m3", "e5m2", f32, seed=M)
+    buf = torch.full((M + 300, N), 7.0, dtype=dtype, device="cuda")
+    ws = cuda_lib.Workspace(256)
+    cuda_lib.gemm_fp8(*args, **kw, out=buf[:M], ws=ws)
+    assert (buf[M:] == 7.0).all() and ws.query() == (0, 0)
+    check_close(num(buf[:M]), ref, err if f32 else err + BF16 * (np.abs(ref) + err), f"{parts} parts")
+    first = buf[:M].clone()
+    for _ in range(3):
+        assert _same(cuda_lib.gemm_fp8(*args, **kw), first)
+
+
+@pytest.mark.parametrize("M,N,K,kw,few,parts", [
+    (65, 256, 2048, {}, False, (4,)), (129, 272, 2064, {}, False, (4,)), (257, 16, 4096, {}, False, (4,)),
+    (8192, 4096, 11008, {}, False, (1,)), (256, 4096, 8192, dict(a_mn_major=True, b_mn_major=True, b_blocks=False), False, (1,)),
+    (64, 4096, 4096, {}, True, (8,)), (1, 16, 16, {}, True, (1,)), (3, 8192, 4096, {}, True, (4,)),
+    # 16 clusters of 8, or 32 of 4, fit into the number of SMs but not into the GPCs of every device.
+    (64, 4096, 4096, dict(b_mn_major=True), False, (3, 4)), (1001, 2048, 3344, dict(b_mn_major=True), False, (1, 2))])
+def test_gemm_parts(cuda_lib, M, N, K, kw, few, parts):
+    got = cuda_lib.gemm_fp8_parts(M, N, K, **kw)
+    assert got[0] == few and got[1] in parts
+
+
 @pytest.mark.parametrize("K", [1, 2, 127, 128, 129, 1000])
 def test_gemm_any_reduction_for_weight_gradients(cuda_lib, K):
     args, kw, ref, err = _gemm_case(cuda_lib, 272, 400, K, True, True, False, "e5m2", "e4m3", True, seed=K)
