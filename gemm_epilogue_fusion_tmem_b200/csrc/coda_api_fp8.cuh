@@ -40,11 +40,14 @@ bool operand8_map(CUtensorMap* m, const void* p, long long mn, long long k, bool
 }
 
 // Few rows of A: the weight becomes the MMA's 128-row operand, the rows its
-// columns (gemm_fp8_skinny_kernel).  Measured at N = K = 4096: 16 rows 6.8 us,
-// 64 rows 9.5 us, where the 256 x 256 tiles, mostly padding, take 16.5 us (65 to
-// 256 rows alike).  With 128 columns the few-rows form took 30 us there.  The
-// gate/up product holds two accumulators and changes over at half the rows (K
-// 4096, F 11008: 64 rows 69 us in the few-rows form, 34 us in tiles).
+// columns (gemm_fp8_skinny_kernel).  Measured at N = K = 4096, few-rows form and
+// 256 x 256 tiles (whose reduction four pairs share): 33 rows 9.4 and 13.3 us, 64
+// rows 9.7 and 13.9; with 128 columns the few-rows form took 30 us where the tiles
+// take 14.  At 64 rows it is ahead or even (2048 x 8192 10.2 and 14.8, 22016 x
+// 4096 26.4 and 32.7, 1024 x 1024 7.2 and 7.4) but for 11008 x 4096 (20.2 and
+// 17.8).  The gate/up product holds two accumulators and changes over at half the
+// rows: K 4096, F 11008, 32 rows 30.8 us in the few-rows form and 34.9 in tiles, 64
+// rows 69 and 34.5; K 2048, F 8192, 32 rows 15.0 and 31.4.
 inline int skinny8_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 
 // Rasterisation as pick_group, in bytes of 8-bit operands.
@@ -108,10 +111,12 @@ coda_status launch_gemm8(const CUtensorMap& ta, const CUtensorMap& tb, Gemm8Para
 // reduction of each is shared by 2 to 4 of them, as many as the device holds at
 // once.  The exchange costs 4 to 5 us, a block of k 0.4: it is done where a pair
 // is spared 12 blocks.  Measured without and with it, N = 2048: 256 rows (4
-// pairs), K 2048 11.1 and 10.7 us, K 8192 29.1 and 16.2; 1001 rows (32 tiles, 2
-// pairs), K 4096 17.9 and 16.7, K 16384 52.8 and 36.3; below the limit, K 2688
-// 13.8 and 14.7.
-// Weight gradients have a tile per 256 x 256 of the weight and fill the device.
+// pairs), K 2048 11.4 and 11.2 us, K 8192 27.5 and 15.9; 1001 rows (32 tiles, 2
+// pairs), K 4096 16.9 and 16.1, K 16384 50.2 and 34.7; below the limit, K 2688
+// 13.5 and 14.3.
+// Weight gradients are not shared: a scale per column needs another layout of the
+// partial tiles.  A weight of fewer than 74 tiles leaves pairs idle (K 8192: 2048 x
+// 2048, 64 tiles, 43 us; 512 x 2048, 16 tiles, 40 us).
 template <int EPI, bool B_MN>
 coda_status activation_parts(long long tiles, int k_blocks, int& parts) {
   for (parts = 4; parts > 1; --parts) {
@@ -214,7 +219,7 @@ coda_status quant8(const QuantParams& p, bool rows, bool cols, bool vec, int gri
   return launch_pass(tag, quant_fp8_kernel<FMT, false, true, false, false>, grid, kQuantThreads, stream, p);
 }
 
-// A row over 256 threads from d = 1025 up: fewer threads of more columns leave
+// A row over 256 threads from d = 1025 to 8192: fewer threads of more columns leave
 // too few loads in flight per SM, more of them wait for one another (8192 rows;
 // 128, 256 and 512 threads: d = 2048 23.6, 22.1 us, -; d = 4096 42.6, 40.0, 42.1
 // us; d = 8192 -, 76.5, 80.6 us).  Wider rows need the registers of more threads.
@@ -228,7 +233,8 @@ constexpr int kRms8MaxD = 1024 * 4 * 8;
 
 // Threads per row of the norm's backward (8 columns each up to d = 8192: with 16
 // columns the next row's loads no longer fit in registers, 67 us against 45 for
-// 8192 x 4096 in L2-warm runs), and its CTAs: a thousand threads per SM, each
+// 8192 x 4096 in L2-warm runs; wider rows, of 16 and 32 columns a thread, spill 56
+// and 416 bytes: 4096 x 16384 110 us, 2048 x 32768 199 us), and its CTAs: a thousand threads per SM, each
 // CTA keeping its share of dg in registers and writing one partial row.
 int rms8_bwd_threads(int d) { return d <= 1024 ? 128 : d <= 2048 ? 256 : d <= 4096 ? 512 : 1024; }
 int rms8_bwd_ctas(int M, int d) { return std::min(M, 148 * (1024 / rms8_bwd_threads(d))); }

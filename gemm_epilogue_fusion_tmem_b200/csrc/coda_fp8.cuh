@@ -143,7 +143,9 @@ __device__ __forceinline__ F2 e4m3_pair(uint32_t w) {
   return f2(v.x, v.y);
 }
 
-// Sigmoids of a pair: 1 / (1 + 2^(-x log2 e)).
+// Sigmoids of a pair: 1 / (1 + 2^(-x log2 e)), with the approximate exponential and
+// reciprocal, since the pass is bound by its instructions: off by at most 6 + 1.2 |x|
+// ulp, the latter from the rounded product x log2 e, four orders below an 8-bit step.
 __device__ __forceinline__ F2 sigmoid2(F2 x) {
   float e0, e1, s0, s1;
   split(x * f2(-1.4426950408889634f, -1.4426950408889634f), e0, e1);
@@ -202,9 +204,11 @@ __device__ __forceinline__ uint2 fp8_pack8(const uint4& q, const F2 (&f)[4]) {
 // meet in shared memory over the 8 warps.  With VEC the matrix is X scaled by
 // rowvec (fp32, rows) and colvec (bf16, columns), which gives the column form of
 // RMSNorm's output from H, r and g without storing it; its maxima are of fp32
-// values, and it takes three CTAs per SM (four spill: 24.2 us for 19.4).
-// Measured at 8192 x 4096, e5m2: rows and columns 22.7 us (5.9 TB/s), columns of
-// H r g 19.4 us (5.2); blocks of 22016 x 4096 42.5 us (6.4).
+// values, and it takes three CTAs per SM (at four the columns form spills, 24.2 us
+// for 19.4 with a warm L2; rows and columns together spill 76 bytes at three).
+// Measured at 8192 x 4096 with a cold L2: rows 18.6 us (5.4 TB/s), rows and columns
+// 24.8 (5.4), columns of H r g 23.2 (4.3), both of H r g 38.5; blocks of 22016 x
+// 4096 42.5 us (6.4).
 constexpr int kQuantThreads = 256;
 constexpr int kQuantRows = 128 * 16 / kQuantThreads;  // rows per thread
 
@@ -497,7 +501,7 @@ struct RmsBwdParams {
 // takes every gridDim.x-th row and keeps sum_i dN_i H_i r_i of its columns in
 // registers, so one pass reads everything once; rmsnorm_fp8_dg_kernel adds the
 // CTAs' partials in a fixed order.  8 bytes per value: 8192 x 4096 with dH_in
-// 51 us (5.2 TB/s) with the reduce; each row's block-wide sum, during which only
+// 51 us (5.2 TB/s) with the reduce (a cold L2); each row's block-wide sum, during which only
 // the next row's loads are in flight, is what keeps it from the copy rate.
 template <int THREADS, int CH>
 __global__ void __launch_bounds__(THREADS) rmsnorm_fp8_bwd_kernel(const RmsBwdParams p) {
@@ -615,8 +619,9 @@ __global__ void __launch_bounds__(kRmsDgThreads)
 // are formed twice, once for the maxima and once to be rounded: keeping them
 // would take 96 registers and half the warps.  Outputs: dA = [da | db] in row
 // blocks (operand of dgrad) and, with COLS, dA and y in column blocks (operands
-// of the two weight gradients).  Measured at 8192 x 11008 with COLS: 200 us (4.1
-// TB/s).  It is bound by its instructions, some 57 per element of which two
+// of the two weight gradients).  Measured at 8190 x 11008: with COLS 200 us (4.1
+// TB/s; 64 registers, 44 to 52 bytes spilled), e5m2 alike, without 143 us (3.8).
+// It is bound by its instructions, some 57 per element of which two
 // exponentials and two reciprocals: the schedulers issue in 73% of the clocks,
 // the special-function unit is 43% busy, DRAM 48%.
 constexpr int kSwBwdThreads = 512;

@@ -16,7 +16,7 @@
 // half's drain has the time of three half-products (768 clocks) to hide the
 // commit, the TMEM reads and the arrival that crosses to the pair's leader.
 // One 256-column product with two buffers was slower (7B down projection 315
-// us against 307).  Half h is columns [128 h, 128 h + 128): 64 rows of B from
+// us against the 307 of the time).  Half h is columns [128 h, 128 h + 128): 64 rows of B from
 // each CTA (the operand's pair order), which makes it one 128-wide scale block
 // of a weight, and in the gate/up product 64 gate columns beside the same 64 up
 // columns.
@@ -29,13 +29,13 @@
 // other two.  Waits are bounded; a role that gives up records it and the CTA
 // drains and exits.
 //
-// Measured, bursts from a cool GPU: M 8192, N 4096, K 11008 in 307-320 us (2310-
-// 2400 TFLOP/s), gate/up SwiGLU 8192 x 4096 x 11008 in 665-683 us (2160-2240),
-// weight gradient 4096 x 4096 x 8192 in 168 us (1640; 3.5 waves of tiles in 4).
-// At 1965 MHz a block of 128 takes about 970 clocks, of which the tensor core
-// works 512: the rest is the round trip of a buffer (drain, arrival, product,
-// commit).  In steady use the 1 kW power cap holds the clock near 1400 MHz and
-// the first of these takes 360-376 us.
+// Measured in steady use: M 8192, N 4096, K 11008 in 357-370 us (2000-2070 TFLOP/s),
+// gate/up SwiGLU 8192 x 4096 x 11008 in 736-749 us (1970-2010), weight gradient 4096 x
+// 4096 x 8191 in 189-192 us (1430-1450; 3.5 waves of tiles in 4).  The 1 kW power cap then holds the clock
+// near 1400 MHz; in bursts from a cool GPU they take 287-310, 612-653 and 159-167
+// us.  At 1965 MHz a block of 128 takes about 920 clocks, of which the tensor core
+// works 512 (its pipe is busy 66-74 % of the time, 44 % with a scale per column):
+// the rest is the round trip of a buffer (drain, arrival, product, commit).
 #pragma once
 
 #include "coda_fp8.cuh"
@@ -705,7 +705,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       for (int left = num_kb; left > 0; left -= F8_GROUP, ++groups) {
         mbar_wait_drain(smem_u32(&sfull[groups & 1]), (groups >> 1) & 1u, wctl, (2 + q) << 8 | kWaitFull);
         // A vote: the lanes come out of the wait one by one while another warp may
-        // be setting the flag, and what follows needs the whole warp.
+        // be setting the flag, and what follows needs the whole warp.  Behind it the
+        // compiler knows the warp converged: the whole kernel takes 4-7 % less time
+        // than with a look at the flag by each lane (gate/up 626 us for 667).
         if (__any_sync(0xffffffffu, *abort_flag)) break;
         const float* sc = sScale + (groups & 1) * GROUP_FLOATS;
         const float* cs = sc + F8_GROUP * 128 + (VEC ? h * 128 + lane % 4 * 2 : EPI == F8_EPI_SWIGLU ? 0 : h);

@@ -422,7 +422,8 @@ coda_status coda_quant_fp8_blocks(const void* W, void* Q, float* S, int R, int C
  * accumulate = 1 the product is added to C (gradient accumulation).
  * Requires N % 16 == 0; K % 16 == 0 unless both operands are MN-major; M % 16 == 0 when a_mn_major.
  * The order of the additions depends on M, N, K and the device, not on the run; added sums below
- * 2^-126 may be flushed to zero.
+ * 2^-126 may be flushed to zero.  The two scales of a block are multiplied first, in fp32: a product
+ * of them below 2^-126 has fewer bits, one above 2^128 is infinite.
  * M = 0 or N = 0 does nothing; K = 0 writes zeros (adds nothing).  ws: coda_gemm_workspace_bytes(). */
 coda_status coda_gemm_fp8(const void* A, const float* SA, const void* B, const float* SB, void* C, int M, int N, int K,
                           int a_mn_major, int b_mn_major, int a_format, int b_format, int b_blocks, int c_fp32,
