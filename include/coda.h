@@ -91,7 +91,8 @@ coda_status coda_shared_status(void** ws);
 
 /* Set the per-wait limit of device-side bounded waits, in nanoseconds, for
  * launches issued after this call from any host thread (default 4e9 = 4 s).
- * Values are clamped to [1e3, 6e10]. */
+ * Values are clamped to [1e3, 6e10].  A kernel that gives up still waits for its
+ * own copies and products in flight, for at least 2 s if it must. */
 void coda_set_wait_limit_ns(uint64_t ns);
 
 /* Self-test of the device-side failure path: a one-warp kernel waits, with
